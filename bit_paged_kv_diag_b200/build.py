@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvq.so")
 SOURCES = ["kvq_api.cu", "append_kernel.cu", "decode_kernel.cu", "kvq_noalloc.cu",
            "prefill_tc.cu"]
-HEADERS = ["kvq_internal.h", "kvq_ptx.cuh"]
+HEADERS = ["kvq_internal.h", "kvq_ptx.cuh", "append_row.cuh", "decode_tile.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
