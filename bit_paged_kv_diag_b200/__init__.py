@@ -8,6 +8,11 @@ The names mirror the C ABI in ``include/kvq.h``:
 * ``kvq_decode_attention``     -> :func:`decode_attention`
 * ``kvq_append_decode_attention`` -> :func:`append_decode_attention`
 * ``kvq_prefill_attention``    -> :func:`prefill_attention`
+* ``kvq_rope_quant_append``    -> :func:`rope_quant_append`
+* ``kvq_gather_rows``          -> :func:`gather_rows`
+* ``kvq_update_block_bounds``  -> :func:`update_block_bounds`
+* ``kvq_select_blocks``        -> :func:`select_blocks`
+* ``kvq_sparse_attention``     -> :func:`sparse_attention`
 * ``kvq_free``                 -> :func:`free`
 * ``kvq_assign_pages``, ``kvq_pool_bytes``, ``kvq_get_device_status`` likewise.
 
@@ -26,6 +31,8 @@ __all__ = [
     "KVQError", "Desc", "Cache", "lib", "pool_bytes", "assign_pages", "alloc_pages",
     "rotate_quant_append", "decode_attention", "append_decode_attention", "prefill_attention",
     "decode_attention_noalloc", "free",
+    "Rope", "BlockBounds", "rope_quant_append", "gather_rows", "update_block_bounds",
+    "select_blocks", "sparse_attention",
     "get_device_status", "status_string",
     "EXPORTED",
 ]
@@ -37,7 +44,8 @@ EXPORTED = (
     "kvq_pool_bytes", "kvq_assign_pages", "kvq_alloc_pages", "kvq_rotate_quant_append",
     "kvq_decode_attention", "kvq_pool_ptr", "kvq_get_device_status", "kvq_free",
     "kvq_status_string", "kvq_decode_attention_noalloc", "kvq_append_decode_attention",
-    "kvq_prefill_attention",
+    "kvq_prefill_attention", "kvq_rope_quant_append", "kvq_gather_rows",
+    "kvq_update_block_bounds", "kvq_select_blocks", "kvq_sparse_attention",
 )
 
 
@@ -72,6 +80,7 @@ def lib() -> ctypes.CDLL:
         path = _build.build()
         L = ctypes.CDLL(path)
         vp, i32, i32p = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)
+        i64 = ctypes.c_int64
         dp = ctypes.POINTER(Desc)
         sig = {
             "kvq_pool_bytes": (ctypes.c_size_t, [dp]),
@@ -91,6 +100,15 @@ def lib() -> ctypes.CDLL:
                                                            ctypes.c_float, vp, vp]),
             "kvq_prefill_attention": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, i32, i32,
                                                      ctypes.c_float, vp, vp]),
+            "kvq_rope_quant_append": (ctypes.c_int, [vp, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp,
+                                                     vp, vp, i32, i32, vp, i32, i32,
+                                                     ctypes.c_double, vp, vp]),
+            "kvq_gather_rows": (ctypes.c_int, [vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp]),
+            "kvq_update_block_bounds": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, vp, i32, i32, vp]),
+            "kvq_select_blocks": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                                 i32, vp, vp]),
+            "kvq_sparse_attention": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32,
+                                                    ctypes.c_float, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -153,10 +171,16 @@ class Cache:
     """Owner of a ``kvq_cache*`` handle.  ``pool`` is the torch tensor backing the pool
     when the caller supplied one (kept alive here)."""
 
-    def __init__(self, handle, desc, pool_tensor):
+    def __init__(self, handle, desc, pool_tensor, device=None):
         self.handle = handle
         self.desc = desc
         self.pool = pool_tensor
+        self.device = device  # index of the CUDA device that the handle was made on
+        # Plain values that every call reads (a ctypes field costs an attribute lookup and a box).
+        self.kv_heads, self.q_heads = desc.num_kv_heads, desc.num_q_heads
+        self.table_width = desc.max_pages_per_seq
+        self.page_shape = (desc.num_layers, desc.num_pages, desc.num_kv_heads)
+        self.torch_device = None if device is None else f"cuda:{device}"
 
     @property
     def pool_ptr(self) -> int:
@@ -195,7 +219,8 @@ def alloc_pages(desc: Desc, capacity_tokens=None, page_order=None, pool=None):
                                orderp, pt.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
                                ctypes.byref(h))
     _check(rc, "kvq_alloc_pages")
-    return Cache(h, desc, pool), pt
+    import torch
+    return Cache(h, desc, pool, torch.cuda.current_device()), pt
 
 
 def rotate_quant_append(cache: Cache, layer: int, k, v, cu_new_tokens, seq_lens, page_table,
@@ -281,6 +306,227 @@ def decode_attention_noalloc(desc: Desc, pool, layer: int, q, seq_lens, page_tab
         _dev_ptr(page_table, "page_table", torch.int32), batch, float(softmax_scale),
         _dev_ptr(out, "out", torch.float16), st, _stream_ptr(stream))
     _check(rc, "kvq_decode_attention_noalloc")
+    return out
+
+
+class Rope:
+    """The position rotation of :func:`rope_quant_append`: ``inv_freq`` fp32 CUDA
+    [rotary_dim / 2] (kept alive here), channel pairs (i, i + rotary_dim / 2) or, interleaved,
+    (2i, 2i + 1); ``factor`` multiplies every cosine and sine."""
+
+    def __init__(self, inv_freq, interleaved=False, factor=1.0):
+        import torch
+        _dev_ptr(inv_freq, "inv_freq", torch.float32)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must have one dimension")
+        self.inv_freq = inv_freq
+        self.rotary_dim = 2 * int(inv_freq.shape[0])
+        self.interleaved = bool(interleaved)
+        self.factor = float(factor)
+
+
+class BlockBounds:
+    """Per-page key bounds of a cache, by pool page: ``codes`` int8 CUDA
+    [num_layers][num_pages][num_kv_heads][2][128] (lower, then upper bounds) in units of
+    ``scale`` fp32 [num_layers][num_pages][num_kv_heads].  Filled by
+    :func:`update_block_bounds`, read by :func:`select_blocks`."""
+
+    def __init__(self, codes, scale):
+        import torch
+        _dev_ptr(codes, "codes", torch.int8)
+        _dev_ptr(scale, "scale", torch.float32)
+        self.codes = codes
+        self.scale = scale
+
+    @classmethod
+    def alloc(cls, cache):
+        """Bounds for every page of ``cache`` (264 bytes per page, KV head and layer)."""
+        import torch
+        shape, dev = cache.page_shape, cache.torch_device
+        return cls(torch.zeros(*shape, 2, 128, dtype=torch.int8, device=dev),
+                   torch.zeros(*shape, dtype=torch.float32, device=dev))
+
+    def pointers(self, cache):
+        import torch
+        shape = cache.page_shape
+        return (_arg(cache, self.codes, "codes", torch.int8, (*shape, 2, 128)),
+                _arg(cache, self.scale, "scale", torch.float32, shape))
+
+
+def _arg(cache, t, what, dtype, shape):
+    """Pointer of a contiguous CUDA tensor on the cache's device, of the given type and shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == cache.device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev_ptr(t, what, dtype)
+    _refuse(cache, t, what, shape)
+
+
+def _refuse(cache, t, what, shape):
+    if t.get_device() != cache.device:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{cache.device}")
+    raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _seqs(cache, seq_lens, page_table, cu, cu_name):
+    """(batch, pointers of seq_lens, page_table and cu) of a call, checked."""
+    import torch
+    i32, batch = torch.int32, seq_lens.shape[0]
+    return (batch, _arg(cache, seq_lens, "seq_lens", i32, (batch,)),
+            _arg(cache, page_table, "page_table", i32, (batch, cache.table_width)),
+            None if cu is None else _arg(cache, cu, cu_name, i32, (batch + 1,)))
+
+
+def _run(cache, stream, name, *args):
+    """Call the library on the cache's device and the given (default: current) stream."""
+    import torch
+    fn = getattr(_lib, name)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(cache.device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == cache.device:
+        rc = fn(cache.handle, *args, stream)
+    else:
+        with torch.cuda.device(cache.device):
+            rc = fn(cache.handle, *args, stream)
+    if rc != KVQ_OK:
+        raise KVQError(name, rc)
+
+
+def _empty(cache, shape, dtype, stream):
+    """An output of the call's stream (so that the allocator orders its reuse after the call)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache.torch_device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=cache.torch_device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=cache.torch_device)
+
+
+def _tokens(cache, t, what, dtype, shape):
+    """(pointer, token stride) of token rows whose heads are contiguous within a token."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == cache.device:
+            s = t.stride()
+            if (s[2] == 1 and (s[1] == 128 or shape[1] == 1)) or shape[0] == 0:
+                return t.data_ptr(), s[0] if shape[0] > 1 else shape[1] * 128
+            raise ValueError(f"{what}: the heads of a token must be contiguous")
+    except AttributeError:
+        pass
+    if getattr(t, "is_cuda", False):
+        if t.dtype != dtype:
+            raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+        _refuse(cache, t, what, shape)
+    raise TypeError(f"{what} must be a CUDA tensor")
+
+
+def _dtype_code(dtype):
+    import torch
+    if dtype == torch.float16:
+        return 0
+    if dtype == torch.bfloat16:
+        return 1
+    raise TypeError(f"rows must be float16 or bfloat16, got {dtype}")
+
+
+def rope_quant_append(cache: Cache, layer: int, k, v, cu_new_tokens, seq_lens, page_table, rope: Rope,
+                      q=None, positions=None, q_out=None, stream=None):
+    """:func:`rotate_quant_append` with the position rotation of q and k applied on the way.
+    k, v [T][Hkv][128] and q [T][Hq][128], all fp16 or all bf16, may be slices of one qkv buffer
+    (a token's heads contiguous, any token stride).  Angles use the cache positions, or
+    ``positions`` int32 [T].  Returns the rotated q in fp16 [T][Hq][128] (None without q)."""
+    import torch
+    T, dtype = k.shape[0], k.dtype
+    code = _dtype_code(dtype)
+    kp, ks = _tokens(cache, k, "k", dtype, (T, cache.kv_heads, 128))
+    vp, vs = _tokens(cache, v, "v", dtype, (T, cache.kv_heads, 128))
+    batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_new_tokens, "cu_new_tokens")
+    pos = None if positions is None else _arg(cache, positions, "positions", torch.int32, (T,))
+    freq = _arg(cache, rope.inv_freq, "inv_freq", torch.float32, (rope.rotary_dim // 2,))
+    qp, qs, op = None, 0, None
+    if q is not None:
+        shape = (T, cache.q_heads, 128)
+        qp, qs = _tokens(cache, q, "q", dtype, shape)
+        if q_out is None:
+            q_out = _empty(cache, shape, torch.float16, stream)
+        op = _arg(cache, q_out, "q_out", torch.float16, shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _run(cache, stream, "kvq_rope_quant_append", int(layer), code, qp, qs, kp, ks, vp, vs, cu, sl, pos, pt,
+         batch, T, freq, rope.rotary_dim, int(rope.interleaved), rope.factor, op)
+    return q_out
+
+
+def gather_rows(cache: Cache, layer: int, cu_rows, starts, page_table, total_rows: int, dtype=None,
+                k_out=None, v_out=None, stream=None):
+    """Cached K and V rows in the model's basis: positions starts[b] .. starts[b] + cu_rows[b+1] -
+    cu_rows[b] - 1 of every sequence, as two tensors [total_rows][Hkv][128] of ``dtype`` (fp16
+    unless given; bf16)."""
+    import torch
+    dtype = torch.float16 if dtype is None else dtype
+    code = _dtype_code(dtype)
+    shape = (int(total_rows), cache.kv_heads, 128)
+    batch, st, pt, cu = _seqs(cache, starts, page_table, cu_rows, "cu_rows")
+    if k_out is None:
+        k_out = _empty(cache, shape, dtype, stream)
+    if v_out is None:
+        v_out = _empty(cache, shape, dtype, stream)
+    _run(cache, stream, "kvq_gather_rows", int(layer), cu, st, pt, batch, shape[0], code,
+         _arg(cache, k_out, "k_out", dtype, shape), _arg(cache, v_out, "v_out", dtype, shape))
+    return k_out, v_out
+
+
+def update_block_bounds(cache: Cache, layer: int, bounds: BlockBounds, cu_new_tokens, seq_lens, page_table,
+                        total_new_tokens: int, stream=None) -> None:
+    """Bounds of every page that an append touched, after that append and with its arguments
+    (seq_lens: the lengths before it)."""
+    batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_new_tokens, "cu_new_tokens")
+    codes, scale = bounds.pointers(cache)
+    _run(cache, stream, "kvq_update_block_bounds", int(layer), codes, scale, cu, sl, pt, batch,
+         int(total_new_tokens))
+
+
+def select_blocks(cache: Cache, layer: int, q, seq_lens, page_table, bounds: BlockBounds, num_blocks: int,
+                  cu_q=None, sink=1, recent=1, blocks=None, stream=None):
+    """Pages to attend per query and KV head: the first ``sink``, the last ``recent`` and the best
+    others by the bounds' score; int32 [total_q][Hkv][num_blocks], ascending, then -1.  q fp16
+    [total_q][Hq][128]; one query per sequence, or the chunks of ``cu_q``.  seq_lens counts the
+    queries' own tokens."""
+    import torch
+    tq, nb = q.shape[0], int(num_blocks)
+    batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_q, "cu_q")
+    codes, scale = bounds.pointers(cache)
+    qp = _arg(cache, q, "q", torch.float16, (tq, cache.q_heads, 128))
+    if blocks is None:
+        blocks = _empty(cache, (tq, cache.kv_heads, max(nb, 0)), torch.int32, stream)
+    bp = _arg(cache, blocks, "blocks", torch.int32, (tq, cache.kv_heads, max(nb, 0)))
+    _run(cache, stream, "kvq_select_blocks", int(layer), codes, scale, qp, cu, sl, pt, batch, tq, nb,
+         int(sink), int(recent), bp)
+    return blocks
+
+
+def sparse_attention(cache: Cache, layer: int, q, seq_lens, page_table, blocks, cu_q=None,
+                     softmax_scale=0.0, out=None, stream=None):
+    """Attention of every query over the pages in its own list: blocks int32
+    [total_q][Hkv][num_blocks] (negative: empty), as :func:`select_blocks` returns it or the
+    caller's own; q, seq_lens, cu_q as there.  Returns fp16 [total_q][Hq][128]."""
+    import torch
+    tq = q.shape[0]
+    batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_q, "cu_q")
+    qp = _arg(cache, q, "q", torch.float16, (tq, cache.q_heads, 128))
+    if blocks.dim() != 3:
+        raise ValueError("blocks must be [total_q][num_kv_heads][num_blocks]")
+    nb = int(blocks.shape[2])
+    bp = _arg(cache, blocks, "blocks", torch.int32, (tq, cache.kv_heads, nb))
+    if out is None:
+        out = _empty(cache, (tq, cache.q_heads, 128), torch.float16, stream)
+    op = _arg(cache, out, "out", torch.float16, (tq, cache.q_heads, 128))
+    _run(cache, stream, "kvq_sparse_attention", int(layer), qp, cu, sl, pt, bp, nb, batch, tq,
+         float(softmax_scale), op)
     return out
 
 

@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
       }
     }
 
-    auto ntok_of = [&](int xx) { return min(kTileTokens, cu.L - (xx - cu.U) * kTileTokens); };
+    auto ntok_of = [&](int xx) { return prefix_valid(min(kTileTokens, cu.L - (xx - cu.U) * kTileTokens)); };
     // Release a consumed slot and refill it with the warp's tile kStages ahead.
     auto refill = [&]() {
       __syncwarp();

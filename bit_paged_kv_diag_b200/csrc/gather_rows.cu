@@ -1,0 +1,270 @@
+// gather_rows.cu -- cached K and V rows read back in the model's basis, for sm_100a.
+//
+// Mathematics.  A row is y = s * n (INT4: n the 4-bit integers, s the row's fp16 scale; NVFP4:
+// n the E2M1 values, s the E4M3 scale of each 16 channels), rotated back by the cache's
+// block-diagonal Hadamard transform, x = c_b * (butterfly of y) -- the orthonormal Sylvester
+// matrix is its own inverse -- and rounded once to fp16 or bf16.  INT4: the butterfly runs on
+// the integers in fp16 pairs, where every sum is exact (|sum| <= 8 * 128 = 2^10), and s * c_b
+// is applied afterwards in fp32 (two roundings of 2^-24 next to the output's 2^-11 or 2^-8).
+// NVFP4: the stages inside a block of 16 channels are exact in fp16 as well (|sum| <= 6 * 16
+// in steps of 1/2); the scales and the stages across blocks are fp32.
+//
+// Layout.  A warp takes the K or the V rows of 16 consecutive tokens of one KV head (1 KB of
+// codes, contiguous inside a page); two lanes hold a row, lane l the channels [64 l, 64 l + 64),
+// so that only b = 128 exchanges data between lanes, and each lane stores whole 32-byte sectors.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "append_row.cuh"
+#include "kvq_internal.h"
+#include "kvq_ptx.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kD = 128;
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRowsPerWarp = 16;
+
+__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t h2sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// (a, c) -> (a + c, a - c) of registers i and i + step, for all pairs with bit `step` of i clear.
+template <int N>
+__device__ __forceinline__ void h2_stage(uint32_t (&x)[N], int step) {
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    if (i & step) continue;
+    const uint32_t a = x[i], c = x[i + step];
+    x[i] = h2add(a, c);
+    x[i + step] = h2sub(a, c);
+  }
+}
+
+// The stage inside a register's pair: (lo, hi) -> (lo + hi, lo - hi).
+template <int N>
+__device__ __forceinline__ void h2_pair_stage(uint32_t (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i++) x[i] = h2fma(x[i], 0xBC003C00u, prmt(x[i], x[i], 0x1032u));  // (1, -1)
+}
+
+// Two fp32 values -> two fp16 or bf16 (lo -> low half), nearest even.
+template <bool BF16>
+__device__ __forceinline__ uint32_t narrow(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void stg_256(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// The lane's 64 channels of an INT4 row: 8 words of codes -> 32 words of outputs.
+template <int BLOCK, bool BF16>
+__device__ __forceinline__ void row_int4(const uint32_t (&w)[8], float f, int l, unsigned pmask, uint32_t (&o)[32]) {
+  // x[4c + s] = channels 8c + s (low half) and 8c + s + 4 (high half)
+  uint32_t x[32];
+#pragma unroll
+  for (int c = 0; c < 8; c++) {
+    x[4 * c] = nib_lo_to_half2(w[c]);
+    x[4 * c + 1] = nib_hi_to_half2(w[c]);
+    x[4 * c + 2] = nib_lo_to_half2(w[c] >> 8);
+    x[4 * c + 3] = nib_hi_to_half2(w[c] >> 8);
+  }
+  if constexpr (BLOCK > 1) {
+    h2_stage(x, 1);
+    h2_stage(x, 2);
+    h2_pair_stage(x);
+#pragma unroll
+    for (int h = 8; h < BLOCK && h < 64; h *= 2) h2_stage(x, h / 2);
+  }
+  if constexpr (BLOCK == 128) {
+    const uint32_t sg = l ? 0xBC00BC00u : 0x3C003C00u;  // lane 0 keeps own + other, lane 1 other - own
+#pragma unroll
+    for (int i = 0; i < 32; i++) x[i] = h2fma(x[i], sg, __shfl_xor_sync(pmask, x[i], 1));
+  }
+#pragma unroll
+  for (int c = 0; c < 8; c++) {
+    float v[8];
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+      v[s] = __fmul_rn(cvt_f16(x[4 * c + s] & 0xFFFFu), f);
+      v[s + 4] = __fmul_rn(cvt_f16(x[4 * c + s] >> 16), f);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++) o[4 * c + e] = narrow<BF16>(v[2 * e], v[2 * e + 1]);
+  }
+}
+
+// The same of an NVFP4 row; sc = the lane's 4 E4M3 scale bytes.
+template <int BLOCK, bool BF16>
+__device__ __forceinline__ void row_fp4(const uint32_t (&w)[8], uint32_t sc, float cb, int l, unsigned pmask,
+                                        uint32_t (&o)[32]) {
+  f2 y[32];  // channels 2i, 2i + 1
+  const float2 s01 = e4m3x2_value(sc & 0xFFFFu), s23 = e4m3x2_value(sc >> 16);
+  const float sv[4] = {s01.x, s01.y, s23.x, s23.y};
+#pragma unroll
+  for (int b = 0; b < 4; b++) {
+    uint32_t x[8];
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+      asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+          : "=r"(x[4 * j]), "=r"(x[4 * j + 1]), "=r"(x[4 * j + 2]), "=r"(x[4 * j + 3])
+          : "r"(w[2 * b + j]));
+    if constexpr (BLOCK > 1) {
+      h2_pair_stage(x);
+      h2_stage(x, 1);
+      h2_stage(x, 2);
+      h2_stage(x, 4);
+    }
+    const f2 S = pk(sv[b], sv[b]);
+#pragma unroll
+    for (int i = 0; i < 8; i++) y[8 * b + i] = mul2(pk(cvt_f16(x[i] & 0xFFFFu), cvt_f16(x[i] >> 16)), S);
+  }
+#pragma unroll
+  for (int h = 16; h < BLOCK && h < 64; h *= 2) {
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      if (i & (h / 2)) continue;
+      const f2 a = y[i], c = y[i + h / 2];
+      y[i] = add2(a, c);
+      y[i + h / 2] = sub2(a, c);
+    }
+  }
+  if constexpr (BLOCK == 128) {
+    const float sg = l ? -1.0f : 1.0f;
+    const f2 SG = pk(sg, sg);
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      float a, c;
+      upk(y[i], a, c);
+      y[i] = fma2(y[i], SG, pk(__shfl_xor_sync(pmask, a, 1), __shfl_xor_sync(pmask, c, 1)));
+    }
+  }
+  const f2 CB = pk(cb, cb);
+#pragma unroll
+  for (int i = 0; i < 32; i++) {
+    float a, c;
+    upk(BLOCK > 1 ? mul2(y[i], CB) : y[i], a, c);
+    o[i] = narrow<BF16>(a, c);
+  }
+}
+
+template <int BLOCK, bool FP4, bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) gather_kernel(GatherParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, l = lane & 1;
+  const unsigned pmask = 0x3u << (lane & 30);
+  // Item: (16 tokens, head, K or V), K or V fastest, then the head.
+  const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int per_group = 2 * p.num_kv_heads;
+  const int tg = item / per_group, rest = item - tg * per_group;
+  const int h = rest >> 1, kv = rest & 1;
+  const int t = tg * kRowsPerWarp + (lane >> 1);
+  if (t >= p.total_rows) return;  // both lanes of a row; nothing below spans more than the pair
+  uint8_t* const out = static_cast<uint8_t*>(kv ? p.v_out : p.k_out);
+  if (!out) return;
+  int lo = 0, hi = p.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.cu_rows + mid) <= t) lo = mid; else hi = mid;
+  }
+  const int first = __ldg(p.cu_rows + lo);
+  if (t < first || t >= __ldg(p.cu_rows + lo + 1)) return;  // a row of no sequence: left as it is
+  const long long pos = static_cast<long long>(__ldg(p.starts + lo)) + (t - first);
+  int page = -1;
+  const bool bad_pos = pos < 0 || (pos >> p.page_shift) >= p.max_pages_per_seq;
+  if (!bad_pos) page = __ldg(p.page_table + static_cast<size_t>(lo) * p.max_pages_per_seq + (pos >> p.page_shift));
+  uint32_t o[32];
+  if (page < 0 || page >= p.num_pages) {
+    atomicOr(p.status, bad_pos ? KVQ_DEV_BAD_POS_BIT : KVQ_DEV_BAD_PAGE_BIT);
+#pragma unroll
+    for (int i = 0; i < 32; i++) o[i] = 0u;
+  } else {
+    constexpr int kScaleBytes = FP4 ? kD / 16 : 2;
+    const int S = p.page_size, slot = static_cast<int>(pos) & (S - 1);
+    const uint8_t* blk = p.pool_layer + (static_cast<size_t>(page) * p.num_kv_heads + h) *
+                                            (static_cast<size_t>(S) * (kD + 2 * kScaleBytes));
+    const uint4* src = reinterpret_cast<const uint4*>(blk + (kv * S + slot) * (kD / 2) + 32 * l);
+    const uint4 a = __ldg(src), b = __ldg(src + 1);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint8_t* sp = blk + S * kD + (kv * S + slot) * kScaleBytes;
+    if constexpr (FP4) {
+      row_fp4<BLOCK, BF16>(w, __ldg(reinterpret_cast<const uint32_t*>(sp) + l), p.cb, l, pmask, o);
+    } else {
+      const float s = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(sp))));
+      row_int4<BLOCK, BF16>(w, BLOCK > 1 ? __fmul_rn(s, p.cb) : s, l, pmask, o);
+    }
+  }
+  uint8_t* dst = out + ((static_cast<size_t>(t) * p.num_kv_heads + h) * kD + 64 * l) * 2;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const uint32_t v[8] = {o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3],
+                           o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]};
+    stg_256(dst + 32 * i, v);
+  }
+}
+
+template <int BLOCK, bool FP4>
+int launch_one(const cudaLaunchConfig_t& cfg, const GatherParams& p, bool bf16) {
+  return (bf16 ? cudaLaunchKernelEx(&cfg, gather_kernel<BLOCK, FP4, true>, p)
+               : cudaLaunchKernelEx(&cfg, gather_kernel<BLOCK, FP4, false>, p)) == cudaSuccess
+             ? 0
+             : -2;
+}
+
+template <bool FP4>
+int launch_block(const cudaLaunchConfig_t& cfg, const GatherParams& p, int block, bool bf16) {
+  switch (block) {
+    case 1: return launch_one<1, FP4>(cfg, p, bf16);
+    case 32: return launch_one<32, FP4>(cfg, p, bf16);
+    case 64: return launch_one<64, FP4>(cfg, p, bf16);
+    case 128: return launch_one<128, FP4>(cfg, p, bf16);
+    default: return -1;
+  }
+}
+
+}  // namespace
+
+int launch_gather(const GatherParams& p, int block, bool fp4, bool bf16, int num_sms, cudaStream_t stream) {
+  (void)num_sms;
+  if (p.total_rows == 0) return 0;
+  const long long items =
+      (static_cast<long long>(p.total_rows) + kRowsPerWarp - 1) / kRowsPerWarp * 2 * p.num_kv_heads;
+  if (items > 0x7fffffffLL - kWarps) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return fp4 ? launch_block<true>(cfg, p, block, bf16) : launch_block<false>(cfg, p, block, bf16);
+}
+
+}  // namespace kvq

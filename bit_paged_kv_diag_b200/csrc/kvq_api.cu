@@ -15,21 +15,6 @@
 #include "../../include/kvq.h"
 #include "kvq_internal.h"
 
-struct kvq_cache {
-  kvq_desc d;
-  uint8_t* pool;
-  size_t pool_bytes;
-  bool own_pool;
-  void* scratch;             // one allocation: status word, unit counters, partials
-  int32_t* status;
-  int32_t* counters;
-  float* part;
-  int device;
-  int num_sms;
-  kvq::DecodeLaunch launch;  // split-pass shape, fixed for the handle
-  float cb;
-};
-
 namespace kvq {
 
 bool desc_valid(const kvq_desc* d, int* why) {
@@ -170,11 +155,12 @@ int kvq_alloc_pages(const kvq_desc* d, void* dev_pool, size_t pool_bytes, int32_
     delete c;
     return KVQ_ECUDA;
   }
-  // Scratch: status word (padded to 256 B), one arrival counter per unit (zero between
-  // calls; the decode kernel resets what it uses), and the per-(unit, CTA, warp) partials
+  // Scratch: status word (padded to 256 B), one arrival counter per unit and per CTA of the
+  // grid (block-sparse attention may count more units than a decode; zero between calls: the
+  // kernels reset what they use), and the per-(unit, CTA, warp) partials
   // [(max_batch * Hkv + grid) * kDecodeWarps * G * kPartStride] fp32.
   const size_t units = static_cast<size_t>(d->max_batch) * d->num_kv_heads;
-  const size_t counter_bytes = (units * 4 + 255) & ~size_t(255);
+  const size_t counter_bytes = ((units + static_cast<size_t>(c->launch.grid)) * 4 + 255) & ~size_t(255);
   const size_t slots = (units + static_cast<size_t>(c->launch.grid)) * kvq::kDecodeWarps;
   const size_t part_bytes = slots * g * kvq::kPartStride * sizeof(float);
   if (cudaMalloc(&c->scratch, 256 + counter_bytes + part_bytes) != cudaSuccess) {

@@ -5,9 +5,28 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kvq.h"
 
 namespace kvq {
+
+// Dynamic shared memory of a kernel raised to `bytes`: an attribute of the function in the
+// current device's context, set once per device (devices 64 and up set it on every launch).
+template <auto Kernel>
+bool ensure_smem(size_t bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if (bit == 0 || (done.load(std::memory_order_acquire) & bit) == 0) {
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
+        cudaSuccess)
+      return false;
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  return true;
+}
 
 // Descriptor validation shared by every entry point that takes a kvq_desc: true when the
 // geometry is one the kernels implement; otherwise *why is KVQ_EINVAL (a null descriptor,
@@ -108,6 +127,113 @@ int launch_append(const AppendParams& p, int block, int num_sms, cudaStream_t st
 // Chunked prefill on the 5th-generation tensor cores (INT4 and NVFP4 caches).
 int launch_prefill_tc(const PrefillParams& p, int total_q, cudaStream_t stream);
 
+// Append with the position rotation of q and k: k, v and q (null: none) fp16 or bf16, token
+// strides in elements.
+struct RopeAppendParams {
+  uint8_t* pool_layer;
+  const void* q;                  // [T] tokens of [Hq][128], or null
+  const void* k;                  // [T] tokens of [Hkv][128]
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* cu_new_tokens;   // [batch+1]
+  const int32_t* seq_lens;        // [batch], before the append
+  const int32_t* positions;       // [T] positions of the angles, or null: the cache positions
+  const int32_t* page_table;
+  const float* inv_freq;          // [rotary_dim / 2]
+  __half* q_out;                  // [T][Hq][128]
+  int32_t* status;
+  double factor;                  // multiplies cosines and sines
+  int rotary_dim;
+  int interleaved;
+  int batch;
+  int total_new_tokens;
+  int num_kv_heads;
+  int group;
+  int num_pages;
+  int page_size;
+  int page_shift;
+  int max_pages_per_seq;
+  float cb;
+  int tile_tokens, tile_heads;    // set by the launcher
+};
+
+// Cached rows back in the model's basis.
+struct GatherParams {
+  const uint8_t* pool_layer;
+  const int32_t* cu_rows;         // [batch+1]
+  const int32_t* starts;          // [batch] first position of each sequence's range
+  const int32_t* page_table;
+  void* k_out;                    // [T][Hkv][128] or null
+  void* v_out;
+  int32_t* status;
+  int batch;
+  int total_rows;
+  int num_kv_heads;
+  int num_pages;
+  int page_size;
+  int page_shift;
+  int max_pages_per_seq;
+  float cb;
+};
+
+// Per-page key bounds.
+struct BoundsParams {
+  const uint8_t* pool_layer;
+  int8_t* codes;                  // [num_pages][Hkv][2][128] of the layer
+  float* scale;                   // [num_pages][Hkv] of the layer
+  const int32_t* cu_new_tokens;
+  const int32_t* seq_lens;        // before the append
+  const int32_t* page_table;
+  int32_t* status;
+  int batch;
+  int total_new_tokens;
+  int num_kv_heads;
+  int num_pages;
+  int page_size;
+  int page_shift;
+  int max_pages_per_seq;
+};
+
+// Pages chosen per query and KV head by the bounds' score.
+struct SelectParams {
+  const int8_t* codes;            // of the layer, as BoundsParams
+  const float* scale;
+  const __half* q;                // [total_q][Hq][128]
+  const int32_t* cu_q;            // [batch+1], or null: one query per sequence
+  const int32_t* seq_lens;        // [batch], the queries' own tokens included
+  const int32_t* page_table;
+  int32_t* blocks;                // [total_q][Hkv][num_blocks]
+  int32_t* status;
+  int batch;
+  int total_q;
+  int num_kv_heads;
+  int group;
+  int num_pages;
+  int page_size;
+  int page_shift;
+  int max_pages_per_seq;
+  int hadamard_block;
+  float cb;
+  int num_blocks, sink, recent;
+  int queries;                    // queries of one CTA's tile (set by the launcher)
+};
+
+struct SparseParams {
+  const int32_t* cu_q;            // [batch+1], or null
+  const int32_t* blocks;          // [total_q][Hkv][num_blocks]
+  int num_blocks;
+  int total_q;
+  int num_counters;               // arrival counters of the handle
+  long long num_slots;            // partial records of G queries in the scratch
+};
+
+// Host-side launchers of the position-rotating append, the read-back, and block-sparse
+// attention with its bounds and selection.
+int launch_rope_append(RopeAppendParams p, int block, bool fp4, bool bf16, int num_sms, cudaStream_t stream);
+int launch_gather(const GatherParams& p, int block, bool fp4, bool bf16, int num_sms, cudaStream_t stream);
+int launch_bounds(const BoundsParams& p, bool fp4, cudaStream_t stream);
+int launch_select(SelectParams p, int num_sms, cudaStream_t stream);
+
 struct DecodeLaunch {
   int grid;          // CTAs (a multiple of the SM count)
   size_t smem;       // dynamic shared memory per CTA
@@ -115,5 +241,22 @@ struct DecodeLaunch {
 // Shape of the decode pass for a batch capacity (grid sized to fill every SM).
 int plan_decode(int group, int page_size, int max_batch, int num_sms, int fp4, DecodeLaunch* out);
 int launch_decode(const DecodeParams& p, const DecodeLaunch& L, cudaStream_t stream);
+// Attention over chosen pages: p as for a decode (batch sequences), sp the queries and lists.
+int launch_sparse(const DecodeParams& p, const SparseParams& sp, int num_sms, cudaStream_t stream);
 
 }  // namespace kvq
+
+struct kvq_cache {
+  kvq_desc d;
+  uint8_t* pool;
+  size_t pool_bytes;
+  bool own_pool;
+  void* scratch;             // one allocation: status word, unit counters, partials
+  int32_t* status;
+  int32_t* counters;
+  float* part;
+  int device;
+  int num_sms;
+  kvq::DecodeLaunch launch;  // split-pass shape, fixed for the handle
+  float cb;
+};

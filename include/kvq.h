@@ -75,7 +75,10 @@
  *     page_table.  These arrays must therefore be complete
  *     when the previous kernel on the stream lets its dependents start.  Kernels that do
  *     not use programmatic launch (PyTorch's, cuBLAS's, copies) only do so by completing,
- *     and this library's own kernels never write these arrays.
+ *     and this library's own kernels never write these arrays.  The calls from
+ *     kvq_rope_quant_append to kvq_sparse_attention wait before they read anything.
+ *   * The current device must be the one the handle was made on; the calls from
+ *     kvq_rope_quant_append to kvq_sparse_attention return KVQ_EINVAL otherwise.
  */
 #ifndef KVQ_H
 #define KVQ_H
@@ -252,6 +255,124 @@ KVQ_API int kvq_prefill_attention(kvq_cache* c, int32_t layer, const void* q,
                                   const int32_t* cu_q, const int32_t* seq_lens,
                                   const int32_t* page_table, int32_t batch, int32_t total_q,
                                   float softmax_scale, void* out, void* stream);
+
+/* Types of rows outside the cache. */
+#define KVQ_DTYPE_FP16 0
+#define KVQ_DTYPE_BF16 1
+
+/* The append of kvq_rotate_quant_append with the position rotation (RoPE) of q and k applied
+ * on the way: one launch that reads q, k and v as the projection left them, rotates q and k by
+ * their positions, writes q' and appends k' and v.
+ *   theta = position * inv_freq[i] (fp64), c = fl32(factor cos theta), s = fl32(factor sin theta)
+ *   x'_a = fl32(fl32(x_a c) - fl32(x_b s)),  x'_b = fl32(fl32(x_b c) + fl32(x_a s))
+ *   (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved, i < rotary_dim / 2;
+ *   channels from rotary_dim on are unchanged.
+ * k' stays fp32 until it is quantised; q' is rounded once to fp16, the type the attention
+ * calls read.
+ *   dtype             KVQ_DTYPE_FP16 or KVQ_DTYPE_BF16, of q, k and v (finite values)
+ *   q, k, v           device [total_new_tokens] tokens of [num_q_heads][128] (q) or
+ *                     [num_kv_heads][128]; a token's heads are contiguous, tokens are
+ *                     q_stride, k_stride, v_stride ELEMENTS apart (a multiple of 8, at least
+ *                     a token's own elements unless there is one token), so that slices of
+ *                     one qkv buffer can be passed; 16-byte aligned.  q may be NULL (then
+ *                     q_out is NULL too)
+ *   cu_new_tokens, seq_lens (BEFORE the append), page_table, batch: as for
+ *                     kvq_rotate_quant_append
+ *   positions         device int32 [total_new_tokens], the positions of the angles, or NULL:
+ *                     the cache positions seq_lens[b] + i
+ *   inv_freq          device fp32 [rotary_dim / 2]
+ *   rotary_dim        16, 32, ..., 128
+ *   factor            multiplies every cosine and sine (1 unless the model scales them)
+ *   q_out             device fp16 [total_new_tokens][num_q_heads][128], 16-byte aligned; must
+ *                     not overlap q, k or v
+ * Tokens behind cu_new_tokens[batch] are ignored: neither the pool nor their rows of q_out are
+ * written.  A bad page or position is flagged and its rows are not stored (its q' still is
+ * written).  Returns KVQ_OK or a negative status (before any launch). */
+KVQ_API int kvq_rope_quant_append(kvq_cache* c, int32_t layer, int32_t dtype, const void* q,
+                                  int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride,
+                                  const int32_t* cu_new_tokens, const int32_t* seq_lens,
+                                  const int32_t* positions, const int32_t* page_table,
+                                  int32_t batch, int32_t total_new_tokens,
+                                  const float* inv_freq, int32_t rotary_dim,
+                                  int32_t interleaved, double factor, void* q_out,
+                                  void* stream);
+
+/* Cached rows read back in the model's basis: dequantised, rotated back and rounded once.
+ *   cu_rows        device int32 [batch+1], cu_rows[0] = 0, non-decreasing: sequence b's rows
+ *                  are cu_rows[b] .. cu_rows[b+1]-1 of the outputs
+ *   starts         device int32 [batch], first position read of each sequence
+ *   total_rows     host int32, rows of the outputs
+ *   dtype          KVQ_DTYPE_FP16 or KVQ_DTYPE_BF16, of the outputs
+ *   k_out, v_out   device [total_rows][num_kv_heads][128], 32-byte aligned; either may be
+ *                  NULL (that half is not read)
+ * Rows behind cu_rows[batch] are left as they were; rows of a bad page or position are flagged
+ * and zeros.  (An INT4 value outside fp16's range becomes infinite in fp16; bf16 holds it.) */
+KVQ_API int kvq_gather_rows(kvq_cache* c, int32_t layer, const int32_t* cu_rows,
+                            const int32_t* starts, const int32_t* page_table, int32_t batch,
+                            int32_t total_rows, int32_t dtype, void* k_out, void* v_out,
+                            void* stream);
+
+/* Per-page bounds of the cached keys, for kvq_select_blocks: for every page that the tokens of
+ * an append touch and every KV head, over the page's filled slots (the cached keys as they are
+ * in the rotated basis),
+ *   hi_d = ceil(max_d / sigma), lo_d = floor(min_d / sigma) as int8, sigma the least power of
+ *   two with 127 sigma >= max_d |.| (0 and zero codes for all-zero keys).
+ *   codes   device int8 [num_layers][num_pages][num_kv_heads][2][128] (lo, then hi), 16-byte
+ *           aligned;  scale  device fp32 [num_layers][num_pages][num_kv_heads] (sigma);
+ *           both owned by the caller and indexed by pool page
+ *   cu_new_tokens, seq_lens (BEFORE the append), page_table, batch, total_new_tokens: those of
+ *           the append, which must have run before on the stream
+ * A page is recomputed whole, so a page that was overwritten or freed and reused needs no
+ * reset.  Nothing else in codes and scale is written. */
+KVQ_API int kvq_update_block_bounds(kvq_cache* c, int32_t layer, void* codes, float* scale,
+                                    const int32_t* cu_new_tokens, const int32_t* seq_lens,
+                                    const int32_t* page_table, int32_t batch,
+                                    int32_t total_new_tokens, void* stream);
+
+/* Pages to attend, per query and KV head: the first `sink` and the last `recent` pages at or
+ * before the query's position, and of the others those with the largest upper bound of q.k,
+ *   score = max over the KV head's query heads g of fl32(I_g s_g) * sigma,
+ *   I_g = sum_d max(c_d, 0) hi_d + min(c_d, 0) lo_d,
+ * where c = rint(y / s), s = fl32(max |y| / 127), y = q rotated with the cache's transform; a
+ * tie goes to the lower page.
+ *   codes, scale   as kvq_update_block_bounds left them
+ *   q              device fp16 [total_q][num_q_heads][128], 16-byte aligned (q' of
+ *                  kvq_rope_quant_append)
+ *   cu_q           device int32 [batch+1], chunk offsets into q; NULL: one query per sequence
+ *                  (total_q = batch).  Query i of a chunk of C_b is at position
+ *                  seq_lens[b] - C_b + i
+ *   seq_lens       device int32 [batch], tokens cached, the queries' own included
+ *   num_blocks     pages per query and KV head (>= 1);  sink + recent <= num_blocks
+ *   blocks         device int32 out [total_q][num_kv_heads][num_blocks]: logical pages
+ *                  (position / page_size) in ascending order, then -1
+ * A sequence shorter than its chunk or beyond its page budget is flagged and its rows are -1;
+ * rows behind cu_q[batch] are left as they were.  max_pages_per_seq up to 50,560 (the scores of
+ * a query stay in shared memory): KVQ_EUNSUPPORTED beyond. */
+KVQ_API int kvq_select_blocks(kvq_cache* c, int32_t layer, const void* codes,
+                              const float* scale, const void* q, const int32_t* cu_q,
+                              const int32_t* seq_lens, const int32_t* page_table,
+                              int32_t batch, int32_t total_q, int32_t num_blocks, int32_t sink,
+                              int32_t recent, int32_t* blocks, void* stream);
+
+/* Attention over chosen pages: each query's heads attend the tokens at or before its position
+ * of the pages in its own list, and read nothing else of the cache.
+ *   q, cu_q, seq_lens, page_table, batch, total_q: as for kvq_select_blocks
+ *   blocks         device int32 [total_q][num_kv_heads][num_blocks], logical pages in any
+ *                  order; negative entries and pages behind the position are empty; a page
+ *                  listed twice counts twice
+ *   num_blocks     >= 1, num_blocks * page_size <= 2^30
+ *   softmax_scale  multiplier of q.k; 0 means 1/sqrt(128)
+ *   out            device fp16 [total_q][num_q_heads][128], 16-byte aligned; zeros where
+ *                  nothing is attended; rows behind cu_q[batch] are left as they were
+ * A sequence shorter than its chunk or beyond its page budget is flagged and its rows are
+ * zeros; a bad page is flagged and left out.  Uses the handle's scratch: calls on one handle
+ * must be ordered (one stream). */
+KVQ_API int kvq_sparse_attention(kvq_cache* c, int32_t layer, const void* q,
+                                 const int32_t* cu_q, const int32_t* seq_lens,
+                                 const int32_t* page_table, const int32_t* blocks,
+                                 int32_t num_blocks, int32_t batch, int32_t total_q,
+                                 float softmax_scale, void* out, void* stream);
 
 /* Decode attention that allocates nothing.  The pages have no counterpart of this call;
  * it exists for callers that cannot call cudaMalloc: an inference runtime that has
