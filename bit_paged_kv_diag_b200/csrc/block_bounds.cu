@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(BoundsParams p) {
   constexpr int kScaleBytes = FP4 ? kD / 16 : 2;
   const uint8_t* blk = p.pool_layer + (static_cast<size_t>(page) * p.num_kv_heads + h) *
                                           (static_cast<size_t>(S) * (kD + 2 * kScaleBytes));
-  const uint16_t* codes = reinterpret_cast<const uint16_t*>(blk) + lane;
+  const unsigned short* codes = reinterpret_cast<const unsigned short*>(blk) + lane;
   const uint8_t* scales = blk + S * kD;
 
   float mx[4], mn[4];
@@ -109,9 +109,9 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(BoundsParams p) {
 #pragma unroll
     for (int i = 0; i < kChunk; i++) {
       const int r = min(r0 + i, filled - 1);  // rows past the end repeat the last one
-      c[i] = __ldg(codes + r * (kD / 4));
-      if constexpr (FP4) s[i] = __ldg(scales + r * kScaleBytes + (lane >> 2));
-      else s[i] = __ldg(reinterpret_cast<const uint16_t*>(scales) + r);
+      c[i] = __ldcg(codes + r * (kD / 4));
+      if constexpr (FP4) s[i] = __ldcg(scales + r * kScaleBytes + (lane >> 2));
+      else s[i] = __ldcg(reinterpret_cast<const unsigned short*>(scales) + r);
     }
 #pragma unroll
     for (int i = 0; i < kChunk; i += 2) {

@@ -11,20 +11,28 @@
 // query's position the first `sink` and the last `recent` are always taken, and the rest by
 // score, a tie going to the lower page; with n <= num_blocks all pages are taken.
 //
-// Scores.  I is a product of the page rows (256 int8: lo, then hi) with the columns of all query
-// heads of a tile (256 int8: min(c, 0), then max(c, 0)): mma.sync m16n8k32 s8 with 16 pages as
-// the M side, read from global memory straight into fragments (a row's 64-byte pieces are whole
-// sectors; a dot product does not depend on the order of its terms, so lane c of a quad takes
-// bytes 64 i + 16 c on).  The scores of a tile's queries over all pages stay in shared memory.
+// Scores.  I is a product of the rows of all query heads of a tile (256 int8: min(c, 0), then
+// max(c, 0)) with the pages' (256 int8: lo, then hi): mma.sync m16n8k32 s8.  Pages are the N side:
+// a fragment is then one register pair of a page's row, and a 32-byte load from global memory is
+// four fragments as it lands (as the M side its registers had to be regrouped for every product,
+// three moves per MMA).  The query rows lie in shared memory in fragment order, one 16-byte load
+// per 4 MMAs.  A dot product does not depend on the order of its terms, so lane c of a quad takes
+// bytes 128 i + 32 c on: a load touches 8 whole 128-byte lines (16-byte loads took three times
+// the passes through the L1 data path, which bounds this phase).  The heads of a query sit in
+// rows R and R + 8, so that half of the maximum over the group stays inside a lane.
 //
-// Choice.  Keys are the scores as ordered 32-bit integers; the k-th largest is found by bisection
-// between the smallest and the largest key, which ends as soon as a threshold leaves exactly k
-// keys, then the pages are written in ascending order by ballots.  A team of warps shares a query.
+// Choice.  Keys are the scores as ordered 32-bit integers.  The k-th largest is found by counting
+// the keys in 256 equal bins between the smallest and the largest, then inside the bin where the
+// k-th falls, and so on: the range shrinks by 2^8 a round, and the search ends as soon as a bin is
+// taken whole, mostly after two rounds (a bisection takes about 20 passes over the keys).  The
+// pages are then written in ascending order from ballot masks.  A team of warps shares a query.
 //
 // Few queries: a cluster of up to 8 CTAs shares the pages of one tile, and its first CTA collects
 // the keys through distributed shared memory and makes the choice.
 #include <cuda_fp16.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "kvq_internal.h"
 #include "kvq_ptx.cuh"
@@ -36,26 +44,44 @@ namespace {
 constexpr int kD = 128;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxQueries = 8;                 // queries of a tile
-constexpr int kColStride = 2 * kD + 16;        // bytes of a column of q codes (bank spread)
+constexpr int kMaxQueries = 16;                // queries of a tile
+constexpr int kBins = 256;
+constexpr float kMagic = 12582912.0f;           // 1.5 * 2^23; |I| <= 127 * 127 * 128 < 2^21
+constexpr int kMagicBits = 0x4B400000;
+constexpr int kRowBytes = 2 * kD;              // bytes of a query head's codes
 constexpr int kMaxCluster = 8;
+constexpr int kTilePages = 32;                 // pages of a warp's step: 4 MMA tiles of 8
 constexpr unsigned kFull = 0xffffffffu;
 
 __host__ __device__ inline int key_words(int pages) { return (pages + 127) / 128 * 128; }
+// Words from one query's keys to the next: 8 queries' stores of the same pages hit different banks.
+__host__ __device__ inline int key_stride(int pages) { return key_words(pages) + 8; }
 
-__host__ __device__ inline int tile_columns(int queries, int group) { return (queries * group + 7) / 8 * 8; }
+// Query heads of a tile, in whole MMA tiles of 16 rows.
+__host__ __device__ inline int tile_rows(int queries, int group) { return (queries * group + 15) / 16 * 16; }
 
 inline size_t select_smem(int queries, int group, int pages) {
-  return static_cast<size_t>(queries) * key_words(pages) * 4 + tile_columns(queries, group) * (kColStride + 4);
+  return static_cast<size_t>(queries) * key_stride(pages) * 4 + tile_rows(queries, group) * (kRowBytes + 4);
 }
 
 constexpr size_t kSmemCap = 200 * 1024;
 
-// Float -> integer of the same order; never 0 (0 marks pages that are not a choice).
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = __float_as_uint(x + 0.0f);  // -0 -> +0
-  const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return k ? k : 1u;
+// Float -> integer of the same order; never 0, which marks the pages that are not a choice.
+// (of fl(x s), s a power of two)
+__device__ __forceinline__ uint32_t ordered(float x, float s) {
+  const int b = __float_as_int(__fmaf_rn(x, s, 0.0f));  // -0 -> +0
+  return max(static_cast<uint32_t>(b ^ ((b >> 31) | static_cast<int>(0x80000000u))), 1u);
+}
+
+// 32 bytes of global memory, as one load.  (Not a read-only load: with programmatic launches the
+// kernel that writes these bytes may run after this one has started.)
+__device__ __forceinline__ u32x8 ldg_256(const void* p) {
+  u32x8 r;
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                 "=r"(r.w[7])
+               : "l"(p));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -81,59 +107,95 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// One query head's int8 codes into its column (and its factor), by one warp.
-__device__ __forceinline__ void prep_column(const __half* row, uint8_t* col, float* sq, int lane,
-                                            const SelectParams& p) {
-  const uint2 raw = __ldg(reinterpret_cast<const uint2*>(row) + lane);  // channels 4 lane ..
-  const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
-  const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
-  float x[4] = {lo.x, lo.y, hi.x, hi.y};
-  if (p.hadamard_block > 1) {
-    const float a0 = __fadd_rn(x[0], x[1]), a1 = __fsub_rn(x[0], x[1]);
-    const float a2 = __fadd_rn(x[2], x[3]), a3 = __fsub_rn(x[2], x[3]);
-    x[0] = __fadd_rn(a0, a2);
-    x[2] = __fsub_rn(a0, a2);
-    x[1] = __fadd_rn(a1, a3);
-    x[3] = __fsub_rn(a1, a3);
-#pragma unroll
-    for (int s = 0; s < 5; s++) {
-      if ((4 << s) < p.hadamard_block) {
-        const float sgn = ((lane >> s) & 1) ? -1.0f : 1.0f;
-#pragma unroll
-        for (int e = 0; e < 4; e++) x[e] = __fmaf_rn(x[e], sgn, __shfl_xor_sync(kFull, x[e], 1 << s));
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; e++) x[e] = __fmul_rn(x[e], p.cb);
-  }
-  float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-  const float s = __fdiv_rn(m, 127.0f);
-  uint32_t neg = 0, pos = 0;
-#pragma unroll
-  for (int e = 0; e < 4; e++) {
-    const int c = s > 0.0f ? static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -127.0f), 127.0f)) : 0;
-    neg |= (static_cast<uint32_t>(min(c, 0)) & 0xFFu) << (8 * e);
-    pos |= (static_cast<uint32_t>(max(c, 0)) & 0xFFu) << (8 * e);
-  }
-  reinterpret_cast<uint32_t*>(col)[lane] = neg;
-  reinterpret_cast<uint32_t*>(col)[32 + lane] = pos;
-  if (lane == 0) *sq = s;
+// Bytes 4 x .. 4 x + 3 of row R of an MMA tile, in fragment order: byte 128 i + 32 c + 8 h + 4 u
+// of a row belongs to k-step 4 i + h, lane 4 (R mod 8) + c, register 2 u + R / 8.
+__device__ __forceinline__ void put_codes(uint32_t* tile, int R, int x, uint32_t v) {
+  const int i = x >> 5, c = (x >> 3) & 3, h = (x >> 1) & 3, u = x & 1;
+  tile[((4 * i + h) * 32 + 4 * (R & 7) + c) * 4 + 2 * u + (R >> 3)] = v;
 }
 
-template <int G>
+// Codes and factors of kBatch query heads at once (their shuffle chains interleave), by one warp;
+// raw[z]: channels 4 lane .. 4 lane + 3 of the head in row i0 + kWarps z of the MMA tiles.
+template <int kBatch>
+__device__ __forceinline__ void prep_rows(const uint2 (&raw)[kBatch], uint32_t* frag, float* sq, int i0, int nrow,
+                                          int lane, const SelectParams& p) {
+  float x[kBatch][4];
+#pragma unroll
+  for (int z = 0; z < kBatch; z++) {
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&raw[z].x));
+    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&raw[z].y));
+    const float a0 = __fadd_rn(lo.x, lo.y), a1 = __fsub_rn(lo.x, lo.y);
+    const float a2 = __fadd_rn(hi.x, hi.y), a3 = __fsub_rn(hi.x, hi.y);
+    const bool rot = p.hadamard_block > 1;
+    x[z][0] = rot ? __fadd_rn(a0, a2) : lo.x;
+    x[z][2] = rot ? __fsub_rn(a0, a2) : hi.x;
+    x[z][1] = rot ? __fadd_rn(a1, a3) : lo.y;
+    x[z][3] = rot ? __fsub_rn(a1, a3) : hi.y;
+  }
+#pragma unroll
+  for (int s = 0; s < 5; s++) {
+    if ((4 << s) < p.hadamard_block) {
+      const float sgn = ((lane >> s) & 1) ? -1.0f : 1.0f;
+#pragma unroll
+      for (int z = 0; z < kBatch; z++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[z][e] = __fmaf_rn(x[z][e], sgn, __shfl_xor_sync(kFull, x[z][e], 1 << s));
+    }
+  }
+  float s[kBatch];
+#pragma unroll
+  for (int z = 0; z < kBatch; z++) {
+    uint32_t mb = 0;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      x[z][e] = __fmul_rn(x[z][e], p.cb);  // (exact for b = 1: c_b = 1)
+      mb = max(mb, __float_as_uint(fabsf(x[z][e])));  // ordered as the values
+    }
+    s[z] = __fdiv_rn(__uint_as_float(__reduce_max_sync(kFull, mb)), 127.0f);
+  }
+#pragma unroll
+  for (int z = 0; z < kBatch; z++) {
+    // c = rint(fl(x / s)) without dividing: t = fl(x fl(1/s)) is within 127 * 3 * 2^-24 < 2^-15 of
+    // the quotient and of its rounding, so rint(t) is rint of it unless t is that near to a half
+    // (then divide).  The low byte of t + 1.5 * 2^23 is rint(t) in two's complement.
+    const float r = s[z] > 0.0f ? __frcp_rn(s[z]) : 0.0f;
+    uint32_t cb[4];
+    float far = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const float t = __fmul_rn(x[z][e], r), m = __fadd_rn(t, kMagic);
+      far = fmaxf(far, fabsf(__fsub_rn(t, __fsub_rn(m, kMagic))));
+      cb[e] = __float_as_uint(m);
+    }
+    if (far > 0.5f - 0x1p-15f) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) cb[e] = __float_as_uint(__fadd_rn(rintf(__fdiv_rn(x[z][e], s[z])), kMagic));
+    }
+    const int i = i0 + z * kWarps;
+    if (i < nrow) {
+      const uint32_t code = prmt(prmt(cb[0], cb[1], 0x0040u), prmt(cb[2], cb[3], 0x0040u), 0x5410u);
+      const uint32_t sign = prmt(code, code, 0xBA98u);  // 0xFF in the bytes of negative codes
+      uint32_t* const tile = frag + (i >> 4) * (16 * kRowBytes / 4);
+      put_codes(tile, i & 15, lane, code & sign);
+      put_codes(tile, i & 15, 32 + lane, code & ~sign);
+      if (lane == 0) sq[i] = s[z];
+    }
+  }
+}
+
+template <int G, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
   griddep_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int red[2][2][kWarps];
+  __shared__ __align__(16) int hist[kWarps][kBins];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const uint32_t C = cluster_size(), rank = cluster_rank();
+  const uint32_t C = CLUSTER ? cluster_size() : 1u, rank = CLUSTER ? cluster_rank() : 0u;
   const int item = blockIdx.x / C, h = blockIdx.y;
-  const int Q = p.queries, KW = key_words(p.max_pages_per_seq);
+  const int Q = p.queries, KW = key_stride(p.max_pages_per_seq);
   uint32_t* const keys = reinterpret_cast<uint32_t*>(smem);              // [Q][KW]
-  uint8_t* const cols = smem + static_cast<size_t>(Q) * KW * 4;          // [columns][kColStride]
-  float* const sq = reinterpret_cast<float*>(cols + tile_columns(Q, G) * kColStride);
+  uint32_t* const frag = keys + static_cast<size_t>(Q) * KW;             // [rows / 16] MMA tiles of 16 query heads
+  float* const sq = reinterpret_cast<float*>(frag + tile_rows(Q, G) * (kRowBytes / 4));
   griddep_wait();
   // The tile's queries t0 .. t0 + nq - 1 of sequence b.  Tile slots as in the bounds kernel:
   // sequence b has those from cu[b] / Q + b on, at least ceil(n / Q) of them.
@@ -154,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
     // (the whole cluster leaves: it shares the item)
     if (nq <= 0 || i0 < 0 || t0 < 0 || t0 + nq > p.total_q) return;
   }
-  const int S = p.page_size, L = __ldg(p.seq_lens + b);
+  const int L = __ldg(p.seq_lens + b);
   const bool bad = L < 0 || static_cast<long long>(L) > (static_cast<long long>(p.max_pages_per_seq) << p.page_shift) ||
                    (p.cu_q && n > L);
   if (bad && tid == 0 && rank == 0) atomicOr(p.status, KVQ_DEV_BAD_POS_BIT);
@@ -167,84 +229,152 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
   // No query of the tile has a choice to make: skip the scores.
   const bool choose = nmax > k;
   if (choose) {
-    const int ncol = nq * G, ncolp = (ncol + 7) / 8 * 8;
-    const __half* qt = p.q + (static_cast<size_t>(t0) * p.num_kv_heads + h) * G * kD;
-    for (int c = w; c < ncolp; c += kWarps) {
-      if (c < ncol) {
-        prep_column(qt + (static_cast<size_t>(c / G) * p.num_kv_heads * G + c % G) * kD, cols + c * kColStride, sq + c,
-                    lane, p);
-      } else {
-        reinterpret_cast<uint32_t*>(cols + c * kColStride)[lane] = 0u;
-        reinterpret_cast<uint32_t*>(cols + c * kColStride)[32 + lane] = 0u;
-        if (lane == 0) sq[c] = 0.0f;
+    const int nrow = tile_rows(nq, G);
+    const int g = lane >> 2, c = lane & 3;
+    const int ntile = (nmax + kTilePages - 1) / kTilePages, step = kWarps * static_cast<int>(C);
+    const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
+    // The first tile's rows are in flight while q is prepared.
+    constexpr int kN = kTilePages / 8;
+    u32x8 rows[kN][2];
+    float sigma[kN];  // of page g of MMA tile r (0: no page there, or a bad one)
+    int pid[kN];  // page g of MMA tile r, a step ahead of the rows
+    auto load_ids = [&](int mt) {
+#pragma unroll
+      for (int r = 0; r < kN; r++) {
+        const int lp = mt * kTilePages + 8 * r + g;
+        pid[r] = lp < nmax ? __ldg(table + lp) : -1;
       }
-    }
+    };
+    auto load_rows = [&](int mt) {
+#pragma unroll
+      for (int r = 0; r < kN; r++) {
+        const bool none = pid[r] < 0 || pid[r] >= p.num_pages;
+        if (none && mt * kTilePages + 8 * r + g < nmax && c == 0) atomicOr(p.status, KVQ_DEV_BAD_PAGE_BIT);
+        const size_t row = static_cast<size_t>(none ? 0 : pid[r]) * p.num_kv_heads + h;
+        const int8_t* src = p.codes + row * (2 * kD) + 32 * c;
+        rows[r][0] = ldg_256(src);
+        rows[r][1] = ldg_256(src + 128);
+        sigma[r] = none ? 0.0f : __ldcg(p.scale + row);
+      }
+    };
+    int mt = static_cast<int>(rank) * kWarps + w;
+    load_ids(mt);
+    if (mt < ntile) load_rows(mt);
+    load_ids(mt + step);
+
+    const __half* qt = p.q + (static_cast<size_t>(t0) * p.num_kv_heads + h) * G * kD;
+    // Row i of the MMA tiles: heads 2 x and 2 x + 1 of a query in rows R and R + 8 (G = 1: a query
+    // each).
+    constexpr int kPairs = G > 1 ? G / 2 : 1;
+    auto query_of = [&](int i) { return G == 1 ? i : (i >> 4) * (16 / G) + (i & 7) / kPairs; };
+    auto prep = [&](auto batch, int i0) {
+      constexpr int kBatch = decltype(batch)::value;
+      uint2 raw[kBatch];
+#pragma unroll
+      for (int z = 0; z < kBatch; z++) {
+        const int i = i0 + z * kWarps, q = query_of(i);
+        const int head = G == 1 ? 0 : 2 * ((i & 7) % kPairs) + ((i >> 3) & 1);
+        raw[z] = make_uint2(0u, 0u);
+        if (i < nrow && q < nq)
+          raw[z] = __ldcg(reinterpret_cast<const uint2*>(qt + (static_cast<size_t>(q) * p.num_kv_heads * G + head) * kD) + lane);
+      }
+      prep_rows<kBatch>(raw, frag, sq, i0, nrow, lane, p);
+    };
+    if (nrow <= 2 * kWarps) prep(std::integral_constant<int, 2>{}, w);
+    else
+      for (int i0 = w; i0 < nrow; i0 += 4 * kWarps) prep(std::integral_constant<int, 4>{}, i0);
     // Keys past the last scored tile of pages count for nothing.
     if (rank == 0) {
-      const int from = (nmax + 15) / 16 * 16, to = key_words(nmax);
+      const int from = ntile * kTilePages, to = key_words(nmax);
       for (int q = 0; q < nq; q++)
         for (int i = from + tid; i < to; i += kThreads) keys[q * KW + i] = 0u;
     }
-    if (C > 1) cluster_sync();  // every CTA of the cluster runs before its memory is written
+    if (CLUSTER) cluster_sync();  // every CTA of the cluster runs before its memory is written
     else __syncthreads();
 
-    const int g = lane >> 2, c = lane & 3;
-    const uint32_t keys0 = C > 1 ? map_rank(smem_addr(keys), 0) : smem_addr(keys);
-    const int ntile = (nmax + 15) / 16, step = kWarps * static_cast<int>(C);
-    const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
-    for (int mt = static_cast<int>(rank) * kWarps + w; mt < ntile; mt += step) {
-      uint4 a[2][4];
-      float sg[2];
-      bool pad[2];
+    const uint32_t keys0 = CLUSTER ? map_rank(smem_addr(keys), 0) : smem_addr(keys);
+    const uint32_t frag_s = smem_addr(frag);
+    for (; mt < ntile; mt += step) {
+      // Sigma of this lane's output pages: 8 r + 2 c and 8 r + 2 c + 1 of the tile.
+      float sg[kN][2];
 #pragma unroll
-      for (int r = 0; r < 2; r++) {
-        const int lp = mt * 16 + g + 8 * r;
-        int page = lp < nmax ? __ldg(table + lp) : -1;
-        pad[r] = page < 0 || page >= p.num_pages;
-        if (pad[r] && lp < nmax && c == 0) atomicOr(p.status, KVQ_DEV_BAD_PAGE_BIT);
-        const size_t row = static_cast<size_t>(pad[r] ? 0 : page) * p.num_kv_heads + h;
-        const uint4* src = reinterpret_cast<const uint4*>(p.codes + row * (2 * kD)) + c;
-#pragma unroll
-        for (int i = 0; i < 4; i++) a[r][i] = __ldg(src + 4 * i);
-        sg[r] = __ldg(p.scale + row);
+      for (int r = 0; r < kN; r++) {
+        sg[r][0] = __shfl_sync(kFull, sigma[r], 8 * c);
+        sg[r][1] = __shfl_sync(kFull, sigma[r], 8 * c + 4);
       }
-      for (int j = 0; j < ncolp / 8; j++) {
-        int acc[4] = {0, 0, 0, 0};
-        const uint4* bc = reinterpret_cast<const uint4*>(cols + (8 * j + g) * kColStride) + c;
+      auto put = [&](int q, int lp, float v, float factor) {
+        if (q >= nq) return;
+        uint32_t key = ordered(v, factor);
+        // (always taken, or behind the query: one unsigned comparison for both ends)
+        if (static_cast<unsigned>(lp - p.sink) >= static_cast<unsigned>(max(pages_of(q) - p.recent - p.sink, 0))) key = 0u;
+        const uint32_t dst = keys0 + static_cast<uint32_t>(q * KW + lp) * 4;
+        if (CLUSTER) st_cluster(dst, key);
+        else sts_32(dst, key);
+      };
+#pragma unroll 1
+      for (int j = 0; j < nrow / 16; j++) {
+        // Sums start at the integer of 1.5 * 2^23: their bits are then the float 1.5 * 2^23 + I.
+        int acc[kN][4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const uint4 bb = bc[4 * i];
-          mma_16832_s8(acc, a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y, bb.x, bb.y);
-          mma_16832_s8(acc, a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w, bb.z, bb.w);
+        for (int r = 0; r < kN; r++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) acc[r][e] = kMagicBits;
+        const uint32_t fr = frag_s + (j * 8 * 32 + lane) * 16;
+#pragma unroll
+        for (int s = 0; s < 8; s++) {
+          const uint4 f = lds_128(fr + s * 512);
+#pragma unroll
+          for (int r = 0; r < kN; r++)
+            mma_16832_s8(acc[r], f.x, f.y, f.z, f.w, rows[r][s >> 2].w[2 * (s & 3)], rows[r][s >> 2].w[2 * (s & 3) + 1]);
         }
-        // Columns 2c, 2c + 1 of row g (acc 0, 1) and g + 8 (acc 2, 3).
-        const float s0 = sq[8 * j + 2 * c], s1 = sq[8 * j + 2 * c + 1];
+        // Rows g (acc 0, 1) and g + 8 (acc 2, 3) of pages 8 r + 2 c, + 1, times the heads' factors.
+        const float s0 = sq[16 * j + g], s1 = sq[16 * j + 8 + g];
+        const uint64_t S0 = f2_pack(s0, s0), S1 = f2_pack(s1, s1), MM = f2_pack(kMagic, kMagic);
+        const int lp0 = mt * kTilePages + 2 * c;
+        const int odd = g & 1, high = (g >> 1) & 1;
+        float t[kN];
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-          float v0 = __fmul_rn(static_cast<float>(acc[2 * r]), s0), v1 = __fmul_rn(static_cast<float>(acc[2 * r + 1]), s1);
-          const int lp = mt * 16 + g + 8 * r;
-          auto put = [&](int q, float v) {
-            if (q >= nq) return;
-            const int np = pages_of(q);
-            uint32_t key = pad[r] ? 1u : ordered(__fmul_rn(v, sg[r]));
-            if (lp < p.sink || lp >= np - p.recent) key = 0u;  // always taken, or past the query
-            const uint32_t dst = keys0 + static_cast<uint32_t>(q * KW + lp) * 4;
-            if (C > 1) st_cluster(dst, key);
-            else sts_32(dst, key);
-          };
+        for (int r = 0; r < kN; r++) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const uint64_t d = f2_sub(f2_pack(__int_as_float(acc[r][e]), __int_as_float(acc[r][e + 1])), MM);
+            const float2 w2 = f2_unpack(f2_mul(d, e ? S1 : S0));
+            v[e] = w2.x;
+            v[e + 1] = w2.y;
+          }
+          const int lp = lp0 + 8 * r;
           if constexpr (G == 1) {
-            put(8 * j + 2 * c, v0);
-            put(8 * j + 2 * c + 1, v1);
+#pragma unroll
+            for (int e = 0; e < 4; e++) put(16 * j + g + (e < 2 ? 0 : 8), lp + (e & 1), v[e], sg[r][e & 1]);
           } else {
-            v0 = fmaxf(v0, v1);
-            if constexpr (G >= 4) v0 = fmaxf(v0, __shfl_xor_sync(kFull, v0, 1));
-            if constexpr (G == 8) v0 = fmaxf(v0, __shfl_xor_sync(kFull, v0, 2));
-            if (c % (G / 2) == 0) put((8 * j + 2 * c) / G, v0);
+            const float u0 = fmaxf(v[0], v[2]), u1 = fmaxf(v[1], v[3]);
+            if constexpr (G == 2) {
+              put(8 * j + g, lp, u0, sg[r][0]);
+              put(8 * j + g, lp + 1, u1, sg[r][1]);
+            } else {
+              // Lanes g and g ^ 1 share a query: the odd one keeps the odd page.
+              const float other = __shfl_xor_sync(kFull, odd ? u0 : u1, 4);
+              t[r] = fmaxf(odd ? u1 : u0, other);
+              if constexpr (G == 4) {
+                put(4 * j + (g >> 1), lp + odd, t[r], odd ? sg[r][1] : sg[r][0]);
+              } else if (r & 1) {
+                // ... and g ^ 2: the one with that bit set keeps the second of two MMA tiles.
+                const float far = __shfl_xor_sync(kFull, high ? t[r - 1] : t[r], 8);
+                const float best = fmaxf(high ? t[r] : t[r - 1], far);
+                const float f = high ? (odd ? sg[r][1] : sg[r][0]) : (odd ? sg[r - 1][1] : sg[r - 1][0]);
+                put(2 * j + (g >> 2), lp - (high ? 0 : 8) + odd, best, f);
+              }
+            }
           }
         }
       }
+      if (mt + step < ntile) {
+        load_rows(mt + step);
+        load_ids(mt + 2 * step);
+      }
     }
-    if (C > 1) cluster_sync();
+    if (CLUSTER) cluster_sync();
     else __syncthreads();
   }
   if (rank != 0) return;
@@ -256,18 +386,21 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
   int parity = 0;
   auto team_sync = [&]() {
     if (TW > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * TW) : "memory");
+    else __syncwarp();
   };
-  // Sum over the team; the two buffers alternate, so one barrier per sum is enough.
-  auto team_sum = [&](int v) {
-    v = __reduce_add_sync(kFull, v);
-    if (TW == 1) return v;
-    if (lane == 0) red[parity][0][w] = v;
+  // Two values per warp, exchanged in the team: f(i, a, b) for its warps i.  The two buffers
+  // alternate, so one barrier per exchange is enough.
+  auto exchange = [&](uint32_t a, uint32_t b, auto&& f) {
+    if (lane == 0) {
+      red[parity][0][w] = static_cast<int>(a);
+      red[parity][1][w] = static_cast<int>(b);
+    }
     team_sync();
-    int s = 0;
-    for (int i = 0; i < TW; i++) s += red[parity][0][team * TW + i];
+    for (int i = 0; i < TW; i++)
+      f(i, static_cast<uint32_t>(red[parity][0][team * TW + i]), static_cast<uint32_t>(red[parity][1][team * TW + i]));
     parity ^= 1;
-    return s;
   };
+  int* const bins = hist[team * TW];
   for (int q = team; q < nq; q += kWarps / TW) {
     const int np = pages_of(q);
     int32_t* out = p.blocks + (static_cast<size_t>(t0 + q) * p.num_kv_heads + h) * k;
@@ -275,113 +408,171 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
       for (int i = tw * 32 + lane; i < k; i += 32 * TW) out[i] = i < np ? i : -1;
       continue;
     }
-    const int want = k - p.sink - p.recent;  // >= 0 (host-checked)
     const uint32_t* kq = keys + q * KW;
     const uint4* kq4 = reinterpret_cast<const uint4*>(kq);
     const int words4 = key_words(np) / 4;
-    // Threshold T: the keys >= T are `want`, or more than that with too few keys >= T + 1.
-    uint32_t T = 0xFFFFFFFFu;
-    int over = 0;  // keys above T
-    bool exact = true;  // exactly `want` keys >= T
-    if (want > 0) {
-      uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
-      for (int i = tw * 32 + lane; i < words4; i += 32 * TW) {
-        const uint4 v = kq4[i];
-        const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+    // f on this team's share of the keys, four at a time (kLoads loads in flight).
+    auto each4 = [&](auto&& f) {
+      constexpr int kLoads = 4;
+      for (int i = tw * 32 + lane; i < words4; i += kLoads * 32 * TW) {
+        uint4 v[kLoads];
 #pragma unroll
-        for (int z = 0; z < 4; z++) {
-          kmax = max(kmax, e[z]);
-          if (e[z]) kmin = min(kmin, e[z]);
-        }
+        for (int z = 0; z < kLoads; z++)
+          v[z] = i + z * 32 * TW < words4 ? kq4[i + z * 32 * TW] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int z = 0; z < kLoads; z++) f(v[z]);
       }
-      kmin = __reduce_min_sync(kFull, kmin);
-      kmax = __reduce_max_sync(kFull, kmax);
-      if (TW > 1) {
-        if (lane == 0) {
-          red[parity][0][w] = static_cast<int>(kmin);
-          red[parity][1][w] = static_cast<int>(kmax);
-        }
+    };
+    // Taken: the pages that always are, the keys >= T, and the first `quota` keys equal to T - 1.
+    uint32_t T = 0xFFFFFFFFu;
+    int quota = 0;
+    int need = k - p.sink - p.recent;  // >= 0 (host-checked), < the keys that are a choice
+    const bool need_any = need > 0;
+    if (need > 0) {
+      uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+      each4([&](uint4 v) {
+        lo = min(min(min(lo, v.x - 1u), min(v.y - 1u, v.z - 1u)), v.w - 1u);  // (0 becomes the largest)
+        hi = max(max(max(hi, v.x), max(v.y, v.z)), v.w);
+      });
+      lo = __reduce_min_sync(kFull, lo);
+      hi = __reduce_max_sync(kFull, hi);
+      if (TW > 1) exchange(lo, hi, [&](int, uint32_t a, uint32_t b2) {
+        lo = min(lo, a);
+        hi = max(hi, b2);
+      });
+      lo += 1u;
+      while (true) {
+        // [lo, hi] in bins of 2^sh keys.
+        const uint32_t width = hi - lo;
+        const int sh = width < kBins ? 0 : 24 - __clz(width);
+        for (int i = tw * 32 + lane; i < kBins; i += 32 * TW) bins[i] = 0;
         team_sync();
-        for (int i = 0; i < TW; i++) {
-          kmin = min(kmin, static_cast<uint32_t>(red[parity][0][team * TW + i]));
-          kmax = max(kmax, static_cast<uint32_t>(red[parity][1][team * TW + i]));
+        each4([&](uint4 v) {
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int z = 0; z < 4; z++)
+            if (e[z] - lo <= width) atomicAdd(bins + ((e[z] - lo) >> sh), 1);
+        });
+        team_sync();
+        // Bins from the top: lane j holds bins 255 - 8 j .. 248 - 8 j.
+        int cnt[8], sum = 0;
+        const int4* b4 = reinterpret_cast<const int4*>(bins) + 62 - 2 * lane;
+        const int4 u0 = b4[1], u1 = b4[0];
+        cnt[0] = u0.w, cnt[1] = u0.z, cnt[2] = u0.y, cnt[3] = u0.x;
+        cnt[4] = u1.w, cnt[5] = u1.z, cnt[6] = u1.y, cnt[7] = u1.x;
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum += cnt[i];
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const int y = __shfl_up_sync(kFull, incl, d);
+          if (lane >= d) incl += y;
         }
-        parity ^= 1;
-      }
-      // count(>= lo) > want, or lo = kmin; count(>= hi) < want; 64-bit for hi = kmax + 1.
-      unsigned long long lo = kmin, hi = static_cast<unsigned long long>(kmax) + 1;
-      exact = false;
-      while (hi - lo > 1) {
-        const uint32_t mid = static_cast<uint32_t>((lo + hi) >> 1);
-        int cnt = 0;
-        for (int i = tw * 32 + lane; i < words4; i += 32 * TW) {
-          const uint4 v = kq4[i];
-          cnt += (v.x >= mid) + (v.y >= mid) + (v.z >= mid) + (v.w >= mid);
+        const int src = __ffs(__ballot_sync(kFull, incl >= need)) - 1;
+        int above = incl - sum, bin = 0, inbin = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          if (inbin == 0 && above + cnt[i] >= need) {
+            bin = 255 - 8 * lane - i;
+            inbin = cnt[i];
+          }
+          if (inbin == 0) above += cnt[i];
         }
-        cnt = team_sum(cnt);
-        if (cnt == want) {
-          lo = mid;
-          exact = true;
+        above = __shfl_sync(kFull, above, src);
+        bin = __shfl_sync(kFull, bin, src);
+        inbin = __shfl_sync(kFull, inbin, src);
+        team_sync();  // the bins are read: the next round may clear them
+        need -= above;
+        lo += static_cast<uint32_t>(bin) << sh;
+        if (inbin == need) {
+          T = lo;
           break;
         }
-        if (cnt > want) lo = mid;
-        else {
-          hi = mid;
-          over = cnt;
+        if (sh == 0) {
+          T = lo + 1u;
+          quota = need;
+          break;
+        }
+        hi = lo + min(hi - lo, (1u << sh) - 1u);
+      }
+    }
+    // The pages in ascending order: each warp of the team a contiguous part; lane i of a warp
+    // holds the mask of the part's pages 32 i .. 32 i + 31.
+    const int words = (np + 31) / 32, per = (words + TW - 1) / TW;
+    const int w0 = tw * per, w1 = min(words, w0 + per);
+    auto masks = [&](int base, uint32_t& sure, uint32_t& tie) {
+      // Bits of the pages below `sink` and from np - recent to np.
+      auto up_to = [&](int n) {  // bits of the lane's word that are pages below n
+        const int m = n - (base + lane) * 32;
+        return m >= 32 ? 0xFFFFFFFFu : m <= 0 ? 0u : (1u << m) - 1u;
+      };
+      uint32_t forced = 0;
+      if (base + lane < w1) forced = up_to(p.sink) | (up_to(np) & ~up_to(np - p.recent));
+      sure = tie = 0;
+      const int m = min(32, w1 - base);
+#pragma unroll 8
+      for (int i = 0; i < m; i++) {
+        const uint32_t key = kq[(base + i) * 32 + lane];
+        const uint32_t ms = __ballot_sync(kFull, key >= T && need_any);
+        if (lane == i) sure = ms;
+        if (quota) {
+          const uint32_t mt = __ballot_sync(kFull, key == T - 1u);
+          if (lane == i) tie = mt;
         }
       }
-      T = static_cast<uint32_t>(lo);
-    }
-    // The pages in ascending order: each warp of the team a contiguous part, 32 pages a step.
-    const int steps = (np + 31) / 32, per = (steps + TW - 1) / TW;
-    const int s0 = tw * per, s1 = min(steps, s0 + per);
-    auto flags = [&](int i, bool& sure, bool& tie) {
-      const uint32_t key = i < np ? kq[i] : 0u;
-      const bool forced = i < np && (i < p.sink || i >= np - p.recent);
-      sure = forced || (want > 0 && key != 0u && (exact ? key >= T : key > T));
-      tie = !exact && want > 0 && !forced && key == T;
+      sure |= forced;
     };
     int before = 0, ties = 0;  // sure and tied pages of the team's earlier warps
+    uint32_t sure = 0, tie = 0;
+    const bool kept = TW > 1 && w1 - w0 <= 32;  // one step: its masks serve both passes
     if (TW > 1) {
-      int cs = 0, ct = 0;
-      for (int s = s0; s < s1; s++) {
-        bool sure, tie;
-        flags(s * 32 + lane, sure, tie);
-        cs += __popc(__ballot_sync(kFull, sure));
-        ct += __popc(__ballot_sync(kFull, tie));
+      uint32_t cs = 0, ct = 0;
+      for (int base = w0; base < w1; base += 32) {
+        masks(base, sure, tie);
+        cs += __reduce_add_sync(kFull, static_cast<unsigned>(__popc(sure)));
+        ct += __reduce_add_sync(kFull, static_cast<unsigned>(__popc(tie)));
       }
-      if (lane == 0) {
-        red[parity][0][w] = cs;
-        red[parity][1][w] = ct;
-      }
-      team_sync();
-      for (int i = 0; i < tw; i++) {
-        before += red[parity][0][team * TW + i];
-        ties += red[parity][1][team * TW + i];
-      }
-      parity ^= 1;
+      exchange(cs, ct, [&](int i, uint32_t a, uint32_t b2) {
+        if (i < tw) {
+          before += static_cast<int>(a);
+          ties += static_cast<int>(b2);
+        }
+      });
     }
-    const int quota = want - over;  // tied pages to take
-    const unsigned below = (1u << lane) - 1u;
-    for (int s = s0; s < s1; s++) {
-      bool sure, tie;
-      flags(s * 32 + lane, sure, tie);
-      const unsigned ms = __ballot_sync(kFull, sure), mt = __ballot_sync(kFull, tie);
-      const bool take = sure || (tie && ties + __popc(mt & below) < quota);
-      if (take) {
-        const int at = before + __popc(ms & below) + min(ties + __popc(mt & below), quota);
-        if (at < k) out[at] = s * 32 + lane;
+    for (int base = w0; base < w1; base += 32) {
+      if (!kept) masks(base, sure, tie);
+      // Exclusive prefixes over the lanes: sure pages low, tied pages high (both below 2^16 in a
+      // step of 1024 pages).
+      const int mine = __popc(sure) | (__popc(tie) << 16);
+      int incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int y = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d) incl += y;
       }
-      before += __popc(ms);
-      ties += __popc(mt);
+      const int total = __shfl_sync(kFull, incl, 31);
+      const int es = before + ((incl - mine) & 0xFFFF), et = ties + ((incl - mine) >> 16);
+      int at = es + min(et, quota), left = quota - et;  // tied pages still to take
+      for (uint32_t m = sure | tie; m; m &= m - 1u) {
+        const int bit = __ffs(m) - 1;
+        if ((tie >> bit) & 1u && left-- <= 0) continue;
+        if (at < k) out[at++] = (base + lane) * 32 + bit;
+      }
+      before += total & 0xFFFF;
+      ties += total >> 16;
     }
   }
 }
 
+template <int G, bool CLUSTER>
+int launch_kernel(cudaLaunchConfig_t& cfg, const SelectParams& p) {
+  if (!ensure_smem<select_kernel<G, CLUSTER>>(kSmemCap)) return -2;
+  return cudaLaunchKernelEx(&cfg, select_kernel<G, CLUSTER>, p) == cudaSuccess ? 0 : -2;
+}
+
 template <int G>
 int launch_one(cudaLaunchConfig_t& cfg, const SelectParams& p) {
-  if (!ensure_smem<select_kernel<G>>(kSmemCap)) return -2;
-  return cudaLaunchKernelEx(&cfg, select_kernel<G>, p) == cudaSuccess ? 0 : -2;
+  return cfg.numAttrs > 1 ? launch_kernel<G, true>(cfg, p) : launch_kernel<G, false>(cfg, p);
 }
 
 }  // namespace
@@ -395,11 +586,10 @@ int launch_select(SelectParams p, int num_sms, cudaStream_t stream) {
   auto tiles = [&](int q) {
     return (p.cu_q ? static_cast<long long>(p.total_q) / q + p.batch : p.batch) * p.num_kv_heads;
   };
-  while (Q > 1 && (select_smem(Q, p.group, p.max_pages_per_seq) > 100 * 1024 || tiles(Q) < num_sms)) Q /= 2;
+  while (Q > 1 && (select_smem(Q, p.group, p.max_pages_per_seq) > 104 * 1024 || tiles(Q) < num_sms)) Q /= 2;
   p.queries = Q;
-  // CTAs that share a tile's pages: while the grid has room for them and each keeps two page
-  // tiles per warp.
-  const int ptiles = (p.max_pages_per_seq + 15) / 16;
+  // CTAs that share a tile's pages: while the grid has room for them and every warp keeps a step.
+  const int ptiles = (p.max_pages_per_seq + kTilePages - 1) / kTilePages;
   int C = 1;
   while (C < kMaxCluster && tiles(Q) * C * 2 <= 2 * num_sms && ptiles >= 2 * kWarps * C) C *= 2;
   const long long items = tiles(Q) / p.num_kv_heads;

@@ -209,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(GatherParams p) {
     const uint8_t* blk = p.pool_layer + (static_cast<size_t>(page) * p.num_kv_heads + h) *
                                             (static_cast<size_t>(S) * (kD + 2 * kScaleBytes));
     const uint4* src = reinterpret_cast<const uint4*>(blk + (kv * S + slot) * (kD / 2) + 32 * l);
-    const uint4 a = __ldg(src), b = __ldg(src + 1);
+    const uint4 a = __ldcg(src), b = __ldcg(src + 1);
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     const uint8_t* sp = blk + S * kD + (kv * S + slot) * kScaleBytes;
     if constexpr (FP4) {
-      row_fp4<BLOCK, BF16>(w, __ldg(reinterpret_cast<const uint32_t*>(sp) + l), p.cb, l, pmask, o);
+      row_fp4<BLOCK, BF16>(w, __ldcg(reinterpret_cast<const uint32_t*>(sp) + l), p.cb, l, pmask, o);
     } else {
-      const float s = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(sp))));
+      const float s = __half2float(__ushort_as_half(__ldcg(reinterpret_cast<const unsigned short*>(sp))));
       row_int4<BLOCK, BF16>(w, BLOCK > 1 ? __fmul_rn(s, p.cb) : s, l, pmask, o);
     }
   }

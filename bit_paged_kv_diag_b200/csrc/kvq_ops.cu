@@ -129,7 +129,7 @@ int kvq_update_block_bounds(kvq_cache* c, int32_t layer, void* codes, float* sca
   if (rc != KVQ_OK) return rc;
   if (total_new_tokens == 0) return KVQ_OK;
   if (batch == 0 || !codes || !scale || !cu_new_tokens || !seq_lens || !page_table) return KVQ_EINVAL;
-  if (!aligned(codes, 16) || !aligned(scale, 4)) return KVQ_EINVAL;
+  if (!aligned(codes, 32) || !aligned(scale, 4)) return KVQ_EINVAL;
   const size_t rows = static_cast<size_t>(layer) * c->d.num_pages * c->d.num_kv_heads;
   kvq::BoundsParams p = {};
   p.pool_layer = layer_of(c, layer);
@@ -159,7 +159,7 @@ int kvq_select_blocks(kvq_cache* c, int32_t layer, const void* codes, const floa
   if (!cu_q && total_q != batch) return KVQ_EINVAL;
   if (batch == 0 || total_q == 0) return KVQ_OK;
   if (!codes || !scale || !q || !seq_lens || !page_table || !blocks) return KVQ_EINVAL;
-  if (!aligned(codes, 16) || !aligned(scale, 4) || !aligned(q, 16)) return KVQ_EINVAL;
+  if (!aligned(codes, 32) || !aligned(scale, 4) || !aligned(q, 16)) return KVQ_EINVAL;  // 256-bit loads
   const size_t rows = static_cast<size_t>(layer) * c->d.num_pages * c->d.num_kv_heads;
   kvq::SelectParams p = {};
   p.codes = static_cast<const int8_t*>(codes) + rows * 256;

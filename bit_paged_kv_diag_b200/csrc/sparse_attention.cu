@@ -60,7 +60,7 @@ __device__ __forceinline__ Entry load_entry(int x, int x1, int lane, const UnitI
   const int j = SEFF < kTileTokens ? x * kPPT + lane % kPPT : (x * kTileTokens) >> p.page_shift;
   if (j >= sp.num_blocks) return e;
   const int off = SEFF < kTileTokens ? 0 : (x * kTileTokens) & (p.page_size - 1);
-  const int blk = __ldg(u.list + j);
+  const int blk = __ldcg(u.list + j);
   if (blk < 0 || blk > (u.pos >> p.page_shift)) return e;  // (an arithmetic shift: -1 stays below 0)
   const int left = u.pos + 1 - (blk << p.page_shift) - off;
   if (left <= 0) return e;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_kernel(DecodeParams p, Spa
   // q of the unit: rotated and cut by all warps.
   {
     const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(t) * p.num_kv_heads + h) * G * kD);
-    for (int i = tid; i < G * kD / 8; i += kThreads) reinterpret_cast<uint4*>(qraw)[i] = __ldg(src + i);
+    for (int i = tid; i < G * kD / 8; i += kThreads) reinterpret_cast<uint4*>(qraw)[i] = __ldcg(src + i);
   }
   __syncthreads();
   prep_q<G, kWarps, FP4>(qraw, frag, sf, lane, p, w);

@@ -318,7 +318,7 @@ KVQ_API int kvq_gather_rows(kvq_cache* c, int32_t layer, const int32_t* cu_rows,
  * in the rotated basis),
  *   hi_d = ceil(max_d / sigma), lo_d = floor(min_d / sigma) as int8, sigma the least power of
  *   two with 127 sigma >= max_d |.| (0 and zero codes for all-zero keys).
- *   codes   device int8 [num_layers][num_pages][num_kv_heads][2][128] (lo, then hi), 16-byte
+ *   codes   device int8 [num_layers][num_pages][num_kv_heads][2][128] (lo, then hi), 32-byte
  *           aligned;  scale  device fp32 [num_layers][num_pages][num_kv_heads] (sigma);
  *           both owned by the caller and indexed by pool page
  *   cu_new_tokens, seq_lens (BEFORE the append), page_table, batch, total_new_tokens: those of
@@ -347,8 +347,9 @@ KVQ_API int kvq_update_block_bounds(kvq_cache* c, int32_t layer, void* codes, fl
  *   blocks         device int32 out [total_q][num_kv_heads][num_blocks]: logical pages
  *                  (position / page_size) in ascending order, then -1
  * A sequence shorter than its chunk or beyond its page budget is flagged and its rows are -1;
- * rows behind cu_q[batch] are left as they were.  max_pages_per_seq up to 50,560 (the scores of
- * a query stay in shared memory): KVQ_EUNSUPPORTED beyond. */
+ * rows behind cu_q[batch] are left as they were; a bad page is flagged and scores 0.
+ * max_pages_per_seq up to 49,920 (the scores of a query stay in shared memory):
+ * KVQ_EUNSUPPORTED beyond. */
 KVQ_API int kvq_select_blocks(kvq_cache* c, int32_t layer, const void* codes,
                               const float* scale, const void* q, const int32_t* cu_q,
                               const int32_t* seq_lens, const int32_t* page_table,
