@@ -3,13 +3,23 @@
 //
 // Mathematics.  Token at position p, pair i of the rotary_dim / 2 rotated channel pairs:
 // theta = p * inv_freq[i] in fp64, c = fl32(factor cos theta), s = fl32(factor sin theta), and
-//   x'_a = fl(fl(x_a c) - fl(x_b s)),  x'_b = fl(fl(x_b c) + fl(x_a s))
+//   x'_a = x_a c - x_b s,  x'_b = x_b c + x_a s
 // with (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) for the interleaved form.  The angle
 // is formed in fp64 because an fp32 product of a far position loses the angle itself (2^17
-// tokens times 1 leaves 2^-7 radian); every rounding above is fixed, so that the stored codes
-// are those of any implementation that rounds the same way.  The rotated k stays in fp32 on its way into the block-diagonal Hadamard
-// butterfly and the quantiser (append_row.cuh), which are the append kernel's; q' is rounded
-// once to fp16, the type that the attention calls read.
+// tokens times 1 leaves 2^-7 radian).  For k both products and the sum round to fp32 one by one,
+// so that the stored codes are those of any implementation that rounds the same way; k' stays in
+// fp32 on its way into the block-diagonal Hadamard butterfly and the quantiser (append_row.cuh),
+// which are the append kernel's.  For q the sum is one fma; q' is rounded once to fp16, the type
+// that the attention calls read.
+//
+// Layout.  A CTA takes a few tokens (of all heads, or of some when the call is short): their K
+// and V rows come by bulk copies into shared memory, the angles of the tokens are computed once
+// for all heads into a table there, and its warps take stages of 16 rows.
+//   q: 8 lanes a row, lane j the two 8-channel chunks of the pairs 8 j .. 8 j + 7, so a pair
+//      never leaves a lane and the cosines stay in registers from row to row; global memory to
+//      registers and back, no shared memory (a row costs 15 warp instructions; two lanes a row,
+//      each computing both partners' products, cost 77).
+//   k, v: two lanes a row, as in the append kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -29,9 +39,9 @@ constexpr int kRow = 2 * kD;          // bytes of one fp16 / bf16 row
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStageRows = 16;        // rows of a warp stage: two lanes per row
-constexpr int kTileRows = 192;        // rows of a CTA's tile, about 48 KB
+constexpr int kTileRows = 128;        // K and V rows of a CTA's tile, about 32 KB
 constexpr int kRopeTokens = 32;       // tokens of a tile at most
-constexpr int kMaxSmem = (kTileRows + 3 * 15) * kRow + kRopeTokens * (kD * 4 + 16) + 16;
+constexpr int kMaxSmem = (kTileRows + 2 * 15) * kRow + kRopeTokens * (kD * 4 + 16) + 16;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bounded waits: 2 s
 
 constexpr int kSlotBadPos = -1, kSlotPadding = -2;
@@ -47,9 +57,41 @@ struct TokenDest {
 __host__ __device__ inline int round16(int n) { return (n + 15) & ~15; }
 
 // Rows of one kind, padded to whole warp stages.
-__host__ __device__ inline size_t tile_smem(int tokens, int heads, int group, bool with_q) {
-  const int nk = round16(tokens * heads), nq = with_q ? round16(tokens * heads * group) : 0;
-  return static_cast<size_t>(2 * nk + nq) * kRow + static_cast<size_t>(tokens) * (2 * (kD / 2) * 4 + sizeof(TokenDest)) + 16;
+__host__ __device__ inline size_t tile_smem(int tokens, int heads) {
+  return static_cast<size_t>(2 * round16(tokens * heads)) * kRow +
+         static_cast<size_t>(tokens) * (2 * (kD / 2) * 4 + sizeof(TokenDest)) + 16;
+}
+
+// cos and sin of theta >= 0 or < 0, |theta| < 2^31, to about 2^-48: theta less the nearest multiple
+// n of pi / 2 (whose first 53 bits and next 53 are subtracted by one fma each, so that r keeps an
+// absolute error of 2^-53), then Taylor's series on |r| <= pi / 4 (first terms left out: r^17 / 17!
+// and r^18 / 18!, below 2^-53), swapped and signed by n mod 4.
+__device__ __forceinline__ void cos_sin(double theta, double& c, double& s) {
+  const double n = rint(theta * 0.63661977236758134308);
+  double r = fma(-n, 1.5707963267948965580, theta);
+  r = fma(-n, 6.1232339957367658861e-17, r);
+  const double z = r * r;
+  double cp = 1.0 / 20922789888000.0, sp = -1.0 / 1307674368000.0;
+  cp = fma(cp, z, -1.0 / 87178291200.0);
+  sp = fma(sp, z, 1.0 / 6227020800.0);
+  cp = fma(cp, z, 1.0 / 479001600.0);
+  sp = fma(sp, z, -1.0 / 39916800.0);
+  cp = fma(cp, z, -1.0 / 3628800.0);
+  sp = fma(sp, z, 1.0 / 362880.0);
+  cp = fma(cp, z, 1.0 / 40320.0);
+  sp = fma(sp, z, -1.0 / 5040.0);
+  cp = fma(cp, z, -1.0 / 720.0);
+  sp = fma(sp, z, 1.0 / 120.0);
+  cp = fma(cp, z, 1.0 / 24.0);
+  sp = fma(sp, z, -1.0 / 6.0);
+  cp = fma(cp, z, -0.5);
+  cp = fma(cp, z, 1.0);
+  sp = fma(sp * z, r, r);
+  const int m = static_cast<int>(static_cast<long long>(n));
+  c = (m & 1) ? sp : cp;
+  s = (m & 1) ? cp : sp;
+  if ((m + 1) & 2) c = -c;
+  if (m & 2) s = -s;
 }
 
 // Two 16-bit values of a word -> fp32 pair, exact.
@@ -104,6 +146,72 @@ __device__ __forceinline__ void rope_row(const uint4 (&raw)[8], uint32_t row, ui
   }
 }
 
+// Stage h = 1 of the butterfly: (a, c) -> (a + c, a - c) inside every pair.
+template <int BLOCK>
+__device__ __forceinline__ void first_stage(f2 (&x)[32]) {
+  if constexpr (BLOCK > 1) {
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      float a, c;
+      upk(x[i], a, c);
+      x[i] = pk(__fadd_rn(a, c), __fsub_rn(a, c));
+    }
+  }
+}
+
+// 16 bytes of global memory that are read once.
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+// 8 values of the inputs' type -> fp16.
+template <bool BF16>
+__device__ __forceinline__ uint4 half_chunk(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    float a, b;
+    upk(widen<BF16>(w[e]), a, b);
+    o[e] = pack_half2(__float2half_rn(a), __float2half_rn(b));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The rotation of two chunks a, b of 8 channels (16-bit values) with the 8 cosines and sines of
+// their pairs: channel e of a with channel e of b, or, interleaved, the pairs inside the chunks.
+template <bool BF16>
+__device__ __forceinline__ void rotate_chunks(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8],
+                                              bool interleaved) {
+  const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+  uint32_t oa[4], ob[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    float a0, a1, b0, b1;
+    upk(widen<BF16>(wa[e]), a0, a1);
+    upk(widen<BF16>(wb[e]), b0, b1);
+    if (!interleaved) {
+      const float y0 = __fmaf_rn(a0, c[2 * e], -__fmul_rn(b0, s[2 * e]));
+      const float y1 = __fmaf_rn(a1, c[2 * e + 1], -__fmul_rn(b1, s[2 * e + 1]));
+      const float z0 = __fmaf_rn(b0, c[2 * e], __fmul_rn(a0, s[2 * e]));
+      const float z1 = __fmaf_rn(b1, c[2 * e + 1], __fmul_rn(a1, s[2 * e + 1]));
+      oa[e] = pack_half2(__float2half_rn(y0), __float2half_rn(y1));
+      ob[e] = pack_half2(__float2half_rn(z0), __float2half_rn(z1));
+    } else {
+      const float y0 = __fmaf_rn(a0, c[e], -__fmul_rn(a1, s[e])), y1 = __fmaf_rn(a1, c[e], __fmul_rn(a0, s[e]));
+      const float z0 = __fmaf_rn(b0, c[4 + e], -__fmul_rn(b1, s[4 + e])), z1 = __fmaf_rn(b1, c[4 + e], __fmul_rn(b0, s[4 + e]));
+      oa[e] = pack_half2(__float2half_rn(y0), __float2half_rn(y1));
+      ob[e] = pack_half2(__float2half_rn(z0), __float2half_rn(z1));
+    }
+  }
+  a = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+  b = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+}
+
 template <int BLOCK, bool FP4, bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendParams p) {
   griddep_launch_dependents();
@@ -113,10 +221,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
   const int h0 = blockIdx.y * p.tile_heads, nh = min(p.tile_heads, p.num_kv_heads - h0);
   const int gq = p.q ? nh * p.group : 0;  // q rows per token of this CTA
   const int nk = nt * nh, nq = nt * gq;
-  // [K rows][V rows][q rows], each padded to 16 rows | cosines and sines | destinations | barrier
-  const uint32_t base = smem_addr(smem);
-  const uint32_t k_s = base, v_s = k_s + round16(nk) * kRow, q_s = v_s + round16(nk) * kRow;
-  uint8_t* const tail = smem + (2 * round16(nk) + round16(nq)) * kRow;
+  // [K rows][V rows], each padded to 16 rows | cosines and sines | destinations | barrier
+  const uint32_t k_s = smem_addr(smem), v_s = k_s + round16(nk) * kRow;
+  uint8_t* const tail = smem + 2 * round16(nk) * kRow;
   float* const cs = reinterpret_cast<float*>(tail);
   TokenDest* const dest = reinterpret_cast<TokenDest*>(cs + nt * kD);
   const uint32_t bar = smem_addr(dest + nt);
@@ -125,18 +232,14 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
     fence_mbar_init();
   }
   griddep_wait();
-  if (tid == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(2 * nk + nq) * kRow);
+  if (tid == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(2 * nk) * kRow);
   __syncthreads();
   // One bulk copy per token and kind: a token's heads are contiguous.
-  for (int i = tid; i < 3 * nt; i += kThreads) {
-    const int kind = i / nt, t = i - kind * nt;
-    if (kind == 2 && nq == 0) continue;
-    const int rows = kind == 2 ? gq : nh;
-    const uint8_t* src = static_cast<const uint8_t*>(kind == 0 ? p.k : kind == 1 ? p.v : p.q);
-    const int64_t stride = kind == 0 ? p.k_stride : kind == 1 ? p.v_stride : p.q_stride;
-    src += (static_cast<int64_t>(t0 + t) * stride) * 2 + static_cast<int64_t>(kind == 2 ? h0 * p.group : h0) * kRow;
-    const uint32_t dst = (kind == 0 ? k_s : kind == 1 ? v_s : q_s) + t * rows * kRow;
-    bulk_copy_g2s(dst, src, rows * kRow, bar, l2_policy_evict_first());
+  for (int i = tid; i < 2 * nt; i += kThreads) {
+    const int kind = i >= nt, t = kind ? i - nt : i;
+    const uint8_t* src = static_cast<const uint8_t*>(kind ? p.v : p.k);
+    src += static_cast<int64_t>(t0 + t) * (kind ? p.v_stride : p.k_stride) * 2 + static_cast<int64_t>(h0) * kRow;
+    bulk_copy_g2s((kind ? v_s : k_s) + t * nh * kRow, src, nh * kRow, bar, l2_policy_evict_first());
   }
   // Each token's sequence, destination and position.
   for (int i = tid; i < nt; i += kThreads) {
@@ -169,10 +272,70 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
   for (int i = tid; i < nt * pairs; i += kThreads) {
     const int t = i / pairs, f = i - t * pairs;
     double s, c;
-    sincos(static_cast<double>(dest[t].pos) * static_cast<double>(__ldg(p.inv_freq + f)), &s, &c);
+    cos_sin(static_cast<double>(dest[t].pos) * static_cast<double>(__ldg(p.inv_freq + f)), c, s);
     cs[t * kD + f] = static_cast<float>(c * p.factor);
     cs[t * kD + kD / 2 + f] = static_cast<float>(s * p.factor);
   }
+  __syncthreads();
+
+  // q: rows r of the tile, token r / gq.  Lane group lane / 8 takes four neighbouring rows of a
+  // stage, all loaded before the first is rotated.
+  const int nsq = (nq + kStageRows - 1) / kStageRows;
+  {
+    const int j = lane & 7, tasks = p.rotary_dim >> 4;
+    const bool turn = j < tasks;
+    const int ca = turn && !p.interleaved ? j : 2 * j, cb = turn && !p.interleaved ? j + tasks : 2 * j + 1;
+    const uint8_t* const q0 = static_cast<const uint8_t*>(p.q) + static_cast<int64_t>(t0) * p.q_stride * 2 +
+                              static_cast<int64_t>(h0) * p.group * kRow;
+    uint8_t* const o0 = reinterpret_cast<uint8_t*>(p.q_out) +
+                        (static_cast<size_t>(t0) * p.num_kv_heads + h0) * p.group * kRow;
+    const size_t o_stride = static_cast<size_t>(p.num_kv_heads) * p.group * kRow;
+    for (int st = w; st < nsq; st += kWarps) {
+      const int r0 = st * kStageRows + 4 * (lane >> 3);
+      int ti = r0 / gq, hq = r0 - ti * gq;
+      uint4 a[4], b[4];
+      uint8_t* dst[4];
+      int tok[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        tok[i] = -1;
+        if (r0 + i < nq) {
+          const uint8_t* src = q0 + static_cast<int64_t>(ti) * p.q_stride * 2 + hq * kRow;
+          a[i] = ldg_stream(src + 16 * ca);
+          b[i] = ldg_stream(src + 16 * cb);
+          dst[i] = o0 + ti * o_stride + hq * kRow;
+          tok[i] = ti;
+          if (++hq == gq) {
+            hq = 0;
+            ti++;
+          }
+        }
+      }
+      float c[8], s[8];
+      int have = -1;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if (tok[i] < 0) continue;
+        if (turn && tok[i] != have) {
+          have = tok[i];
+          const float4* src = reinterpret_cast<const float4*>(cs + have * kD + 8 * j);
+          const float4 c0 = src[0], c1 = src[1], s0 = src[kD / 8], s1 = src[kD / 8 + 1];
+          c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+          s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+        }
+        if (turn) {
+          rotate_chunks<BF16>(a[i], b[i], c, s, p.interleaved);
+        } else if (BF16) {  // unrotated channels: only the type changes
+          a[i] = half_chunk<BF16>(a[i]);
+          b[i] = half_chunk<BF16>(b[i]);
+        }
+        if (dest[tok[i]].slot == kSlotPadding) continue;
+        stg_128(dst[i] + 16 * ca, a[i].x, a[i].y, a[i].z, a[i].w);
+        stg_128(dst[i] + 16 * cb, b[i].x, b[i].y, b[i].z, b[i].w);
+      }
+    }
+  }
+
   const bool landed = mbar_wait_bounded(bar, 0, kWaitLimitNs);
   if (!landed) {
     // Flag it; give the copies in flight another bounded wait before the CTA may exit.
@@ -183,76 +346,39 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
 
   const int l = lane & 1, rho = lane & 7;
   const unsigned pmask = 0x3u << (lane & 30);
-  const int nsk = round16(nk) / kStageRows, nsq = round16(nq) / kStageRows;
+  const int nsk = round16(nk) / kStageRows;
   const uint32_t cs_s = smem_addr(cs);
-  for (int st = w; st < 2 * nsk + nsq; st += kWarps) {
-    const int kind = st < nsk ? 0 : st < 2 * nsk ? 1 : 2;
-    const int r = (st - (kind == 0 ? 0 : kind == 1 ? nsk : 2 * nsk)) * kStageRows + (lane >> 1);
-    const uint32_t row = (kind == 0 ? k_s : kind == 1 ? v_s : q_s) + r * kRow;
-    const bool active = r < (kind == 2 ? nq : nk);
+  // (the warps that had a q stage less start here)
+  for (int st = (w + nsq) % kWarps; st < 2 * nsk; st += kWarps) {
+    const int kind = st >= nsk;
+    const int r = (kind ? st - nsk : st) * kStageRows + (lane >> 1);
+    const uint32_t row = (kind ? v_s : k_s) + r * kRow;
+    const bool active = r < nk;
     uint4 raw[8];
     f2 x[32];
     int ti = 0;
     if (active) {  // both lanes of a row take the same branch
-      ti = r / (kind == 2 ? gq : nh);
+      ti = r / nh;
 #pragma unroll
       for (int t = 0; t < 8; t++) raw[t] = lds_128(row + kD * l + 16 * (t ^ rho));
-    }
-    if (kind == 2) {
-      uint32_t o[32];
-      if (active) {
-        rope_row<BF16>(raw, row, cs_s + ti * (kD * 4), rho, l, p, x);
-#pragma unroll
-        for (int i = 0; i < 32; i++) {
-          float a, b;
-          upk(x[i], a, b);
-          o[i] = pack_half2(__float2half_rn(a), __float2half_rn(b));
-        }
-      }
-      // Back into the row's place (both lanes have read both halves), then out in whole rows.
-      __syncwarp();
-      if (active) {
-#pragma unroll
-        for (int t = 0; t < 8; t++)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + kD * l + 16 * (t ^ rho)), "r"(o[4 * t]),
-                       "r"(o[4 * t + 1]), "r"(o[4 * t + 2]), "r"(o[4 * t + 3])
-                       : "memory");
-      }
-      __syncwarp();
-      const int r0 = (st - 2 * nsk) * kStageRows;
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const int rr = r0 + 2 * i + (lane >> 4);
-        if (rr >= nq) continue;
-        const int tt = rr / gq;
-        if (dest[tt].slot == kSlotPadding) continue;
-        const uint4 v = lds_128(q_s + rr * kRow + 16 * (lane & 15));
-        __half* dst = p.q_out + (static_cast<size_t>(t0 + tt) * p.num_kv_heads * p.group + h0 * p.group + (rr - tt * gq)) * kD;
-        stg_128(reinterpret_cast<uint8_t*>(dst) + 16 * (lane & 15), v.x, v.y, v.z, v.w);
-      }
-      continue;
     }
     if (active) {
       if (kind == 0) {
         rope_row<BF16>(raw, row, cs_s + ti * (kD * 4), rho, l, p, x);
-      } else {
+        first_stage<BLOCK>(x);
+        rotate_stages<BLOCK>(rho, l, pmask, x);
+      } else if constexpr (BF16) {
 #pragma unroll
         for (int t = 0; t < 8; t++) {
           const uint32_t wd[4] = {raw[t].x, raw[t].y, raw[t].z, raw[t].w};
 #pragma unroll
           for (int e = 0; e < 4; e++) x[4 * t + e] = widen<BF16>(wd[e]);
         }
+        first_stage<BLOCK>(x);
+        rotate_stages<BLOCK>(rho, l, pmask, x);
+      } else {
+        rotate_row<BLOCK>(raw, rho, l, pmask, x);
       }
-      if constexpr (BLOCK > 1) {
-        // Stage h = 1: (a, c) -> (a + c, a - c).
-#pragma unroll
-        for (int i = 0; i < 32; i++) {
-          float a, c;
-          upk(x[i], a, c);
-          x[i] = pk(__fadd_rn(a, c), __fsub_rn(a, c));
-        }
-      }
-      rotate_stages<BLOCK>(rho, l, pmask, x);
       uint32_t q[8], sbits;
       if constexpr (FP4) sbits = quantise_fp4(x, p.cb, rho, q);
       else sbits = quantise(x, p.cb, pmask, q);
@@ -300,10 +426,9 @@ int launch_block(const cudaLaunchConfig_t& cfg, const RopeAppendParams& p, int b
 
 int launch_rope_append(RopeAppendParams p, int block, bool fp4, bool bf16, int num_sms, cudaStream_t stream) {
   if (p.total_new_tokens == 0) return 0;
-  const int per_head = 2 + (p.q ? p.group : 0);
-  int heads = kTileRows / per_head;
+  int heads = kTileRows / 2;
   if (heads > p.num_kv_heads) heads = p.num_kv_heads;
-  int tokens = kTileRows / (per_head * heads);
+  int tokens = kTileRows / (2 * heads);
   if (tokens > kRopeTokens) tokens = kRopeTokens;
   // A short call is spread over the SMs: tiles of fewer tokens, then of fewer heads.
   auto ctas = [&] {
@@ -317,7 +442,7 @@ int launch_rope_append(RopeAppendParams p, int block, bool fp4, bool bf16, int n
   cfg.gridDim = dim3((p.total_new_tokens + tokens - 1) / tokens, (p.num_kv_heads + heads - 1) / heads);
   if (cfg.gridDim.y > 65535) return -1;
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = tile_smem(tokens, heads, p.group, p.q != nullptr);
+  cfg.dynamicSmemBytes = tile_smem(tokens, heads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -264,7 +264,7 @@ KVQ_API int kvq_prefill_attention(kvq_cache* c, int32_t layer, const void* q,
  * on the way: one launch that reads q, k and v as the projection left them, rotates q and k by
  * their positions, writes q' and appends k' and v.
  *   theta = position * inv_freq[i] (fp64), c = fl32(factor cos theta), s = fl32(factor sin theta)
- *   x'_a = fl32(fl32(x_a c) - fl32(x_b s)),  x'_b = fl32(fl32(x_b c) + fl32(x_a s))
+ *   x'_a = x_a c - x_b s,  x'_b = x_b c + x_a s  in fp32 (k: every operation rounded)
  *   (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved, i < rotary_dim / 2;
  *   channels from rotary_dim on are unchanged.
  * k' stays fp32 until it is quantised; q' is rounded once to fp16, the type the attention
