@@ -11,7 +11,11 @@
 //
 // Layout.  A warp takes the K or the V rows of 16 consecutive tokens of one KV head (1 KB of
 // codes, contiguous inside a page); two lanes hold a row, lane l the channels [64 l, 64 l + 64),
-// so that only b = 128 exchanges data between lanes, and each lane stores whole 32-byte sectors.
+// so that only b = 128 exchanges data between lanes.  The finished rows go through shared memory
+// and leave by one bulk copy each: stored from registers, a lane's 128 bytes are a line of their
+// own in every store and the L1 data path takes 32 passes per kilobyte.  Slot t of lane l holds
+// the chunk (8 channels) t ^ 4 l, so that with rows 272 bytes apart the lanes' 16-byte stores hit
+// all banks evenly; the stage h = 32 and the exchange of h = 64 account for that order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -28,6 +32,7 @@ constexpr int kD = 128;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowsPerWarp = 16;
+constexpr int kRowStride = 2 * kD + 16;  // bytes between rows in shared memory
 
 __device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -73,13 +78,15 @@ __device__ __forceinline__ uint32_t narrow(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ void stg_256(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+// 1-D bulk copy of this CTA's shared memory to global memory (16-byte aligned, whole 16-byte
+// units), and the wait until the copies' reads of shared memory are done.
+__device__ __forceinline__ void bulk_copy_s2g(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
-// The lane's 64 channels of an INT4 row: 8 words of codes -> 32 words of outputs.
+// The lane's 64 channels of an INT4 row: 8 words of codes (slot order) -> 32 words of outputs.
 template <int BLOCK, bool BF16>
 __device__ __forceinline__ void row_int4(const uint32_t (&w)[8], float f, int l, unsigned pmask, uint32_t (&o)[32]) {
   // x[4c + s] = channels 8c + s (low half) and 8c + s + 4 (high half)
@@ -95,13 +102,27 @@ __device__ __forceinline__ void row_int4(const uint32_t (&w)[8], float f, int l,
     h2_stage(x, 1);
     h2_stage(x, 2);
     h2_pair_stage(x);
+    h2_stage(x, 4);
+    h2_stage(x, 8);
+  }
+  const uint32_t sg = l ? 0xBC00BC00u : 0x3C003C00u, nsg = l ? 0x3C003C00u : 0xBC00BC00u;
+  if constexpr (BLOCK >= 64) {
+    // h = 32: slots t and t + 4; in lane 1 slot t is the upper chunk.
 #pragma unroll
-    for (int h = 8; h < BLOCK && h < 64; h *= 2) h2_stage(x, h / 2);
+    for (int i = 0; i < 16; i++) {
+      const uint32_t a = x[i], c = x[i + 16];
+      x[i] = h2fma(a, sg, c);
+      x[i + 16] = h2fma(c, nsg, a);
+    }
   }
   if constexpr (BLOCK == 128) {
-    const uint32_t sg = l ? 0xBC00BC00u : 0x3C003C00u;  // lane 0 keeps own + other, lane 1 other - own
+    // h = 64: lane 0 keeps own + other, lane 1 other - own; the partner of slot t is slot t ^ 4.
 #pragma unroll
-    for (int i = 0; i < 32; i++) x[i] = h2fma(x[i], sg, __shfl_xor_sync(pmask, x[i], 1));
+    for (int i = 0; i < 16; i++) {
+      const uint32_t ra = __shfl_xor_sync(pmask, x[i + 16], 1), rc = __shfl_xor_sync(pmask, x[i], 1);
+      x[i] = h2fma(x[i], sg, ra);
+      x[i + 16] = h2fma(x[i + 16], sg, rc);
+    }
   }
 #pragma unroll
   for (int c = 0; c < 8; c++) {
@@ -116,7 +137,7 @@ __device__ __forceinline__ void row_int4(const uint32_t (&w)[8], float f, int l,
   }
 }
 
-// The same of an NVFP4 row; sc = the lane's 4 E4M3 scale bytes.
+// The same of an NVFP4 row; sc = the lane's 4 E4M3 scale bytes in slot order.
 template <int BLOCK, bool BF16>
 __device__ __forceinline__ void row_fp4(const uint32_t (&w)[8], uint32_t sc, float cb, int l, unsigned pmask,
                                         uint32_t (&o)[32]) {
@@ -143,24 +164,35 @@ __device__ __forceinline__ void row_fp4(const uint32_t (&w)[8], uint32_t sc, flo
 #pragma unroll
     for (int i = 0; i < 8; i++) y[8 * b + i] = mul2(pk(cvt_f16(x[i] & 0xFFFFu), cvt_f16(x[i] >> 16)), S);
   }
+  if constexpr (BLOCK > 1) {
 #pragma unroll
-  for (int h = 16; h < BLOCK && h < 64; h *= 2) {
-#pragma unroll
-    for (int i = 0; i < 32; i++) {
-      if (i & (h / 2)) continue;
-      const f2 a = y[i], c = y[i + h / 2];
+    for (int i = 0; i < 32; i++) {  // h = 16
+      if (i & 8) continue;
+      const f2 a = y[i], c = y[i + 8];
       y[i] = add2(a, c);
-      y[i + h / 2] = sub2(a, c);
+      y[i + 8] = sub2(a, c);
+    }
+  }
+  const float sg = l ? -1.0f : 1.0f;
+  const f2 SG = pk(sg, sg), NSG = pk(-sg, -sg);
+  if constexpr (BLOCK >= 64) {
+#pragma unroll
+    for (int i = 0; i < 16; i++) {  // h = 32
+      const f2 a = y[i], c = y[i + 16];
+      y[i] = fma2(a, SG, c);
+      y[i + 16] = fma2(c, NSG, a);
     }
   }
   if constexpr (BLOCK == 128) {
-    const float sg = l ? -1.0f : 1.0f;
-    const f2 SG = pk(sg, sg);
 #pragma unroll
-    for (int i = 0; i < 32; i++) {
-      float a, c;
-      upk(y[i], a, c);
-      y[i] = fma2(y[i], SG, pk(__shfl_xor_sync(pmask, a, 1), __shfl_xor_sync(pmask, c, 1)));
+    for (int i = 0; i < 16; i++) {  // h = 64
+      float a0, a1, c0, c1;
+      upk(y[i], a0, a1);
+      upk(y[i + 16], c0, c1);
+      const f2 ra = pk(__shfl_xor_sync(pmask, c0, 1), __shfl_xor_sync(pmask, c1, 1));
+      const f2 rc = pk(__shfl_xor_sync(pmask, a0, 1), __shfl_xor_sync(pmask, a1, 1));
+      y[i] = fma2(y[i], SG, ra);
+      y[i + 16] = fma2(y[i + 16], SG, rc);
     }
   }
   const f2 CB = pk(cb, cb);
@@ -174,57 +206,71 @@ __device__ __forceinline__ void row_fp4(const uint32_t (&w)[8], uint32_t sc, flo
 
 template <int BLOCK, bool FP4, bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) gather_kernel(GatherParams p) {
+  __shared__ __align__(128) uint8_t stage[kWarps][kRowsPerWarp * kRowStride];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, l = lane & 1;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, l = lane & 1;
   const unsigned pmask = 0x3u << (lane & 30);
   // Item: (16 tokens, head, K or V), K or V fastest, then the head.
-  const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int item = blockIdx.x * kWarps + w;
   const int per_group = 2 * p.num_kv_heads;
   const int tg = item / per_group, rest = item - tg * per_group;
   const int h = rest >> 1, kv = rest & 1;
   const int t = tg * kRowsPerWarp + (lane >> 1);
-  if (t >= p.total_rows) return;  // both lanes of a row; nothing below spans more than the pair
   uint8_t* const out = static_cast<uint8_t*>(kv ? p.v_out : p.k_out);
-  if (!out) return;
-  int lo = 0, hi = p.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.cu_rows + mid) <= t) lo = mid; else hi = mid;
-  }
-  const int first = __ldg(p.cu_rows + lo);
-  if (t < first || t >= __ldg(p.cu_rows + lo + 1)) return;  // a row of no sequence: left as it is
-  const long long pos = static_cast<long long>(__ldg(p.starts + lo)) + (t - first);
-  int page = -1;
-  const bool bad_pos = pos < 0 || (pos >> p.page_shift) >= p.max_pages_per_seq;
-  if (!bad_pos) page = __ldg(p.page_table + static_cast<size_t>(lo) * p.max_pages_per_seq + (pos >> p.page_shift));
-  uint32_t o[32];
-  if (page < 0 || page >= p.num_pages) {
-    atomicOr(p.status, bad_pos ? KVQ_DEV_BAD_POS_BIT : KVQ_DEV_BAD_PAGE_BIT);
+  bool have = out != nullptr && t < p.total_rows;  // (the same in both lanes of a row)
+  if (have) {
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.cu_rows + mid) <= t) lo = mid; else hi = mid;
+    }
+    const int first = __ldg(p.cu_rows + lo);
+    have = t >= first && t < __ldg(p.cu_rows + lo + 1);  // otherwise a row of no sequence: left as it is
+    if (have) {
+      const long long pos = static_cast<long long>(__ldg(p.starts + lo)) + (t - first);
+      int page = -1;
+      const bool bad_pos = pos < 0 || (pos >> p.page_shift) >= p.max_pages_per_seq;
+      if (!bad_pos) page = __ldg(p.page_table + static_cast<size_t>(lo) * p.max_pages_per_seq + (pos >> p.page_shift));
+      uint32_t o[32];
+      if (page < 0 || page >= p.num_pages) {
+        atomicOr(p.status, bad_pos ? KVQ_DEV_BAD_POS_BIT : KVQ_DEV_BAD_PAGE_BIT);
 #pragma unroll
-    for (int i = 0; i < 32; i++) o[i] = 0u;
-  } else {
-    constexpr int kScaleBytes = FP4 ? kD / 16 : 2;
-    const int S = p.page_size, slot = static_cast<int>(pos) & (S - 1);
-    const uint8_t* blk = p.pool_layer + (static_cast<size_t>(page) * p.num_kv_heads + h) *
-                                            (static_cast<size_t>(S) * (kD + 2 * kScaleBytes));
-    const uint4* src = reinterpret_cast<const uint4*>(blk + (kv * S + slot) * (kD / 2) + 32 * l);
-    const uint4 a = __ldcg(src), b = __ldcg(src + 1);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const uint8_t* sp = blk + S * kD + (kv * S + slot) * kScaleBytes;
-    if constexpr (FP4) {
-      row_fp4<BLOCK, BF16>(w, __ldcg(reinterpret_cast<const uint32_t*>(sp) + l), p.cb, l, pmask, o);
-    } else {
-      const float s = __half2float(__ushort_as_half(__ldcg(reinterpret_cast<const unsigned short*>(sp))));
-      row_int4<BLOCK, BF16>(w, BLOCK > 1 ? __fmul_rn(s, p.cb) : s, l, pmask, o);
+        for (int i = 0; i < 32; i++) o[i] = 0u;
+      } else {
+        constexpr int kScaleBytes = FP4 ? kD / 16 : 2;
+        const int S = p.page_size, slot = static_cast<int>(pos) & (S - 1);
+        const uint8_t* blk = p.pool_layer + (static_cast<size_t>(page) * p.num_kv_heads + h) *
+                                                (static_cast<size_t>(S) * (kD + 2 * kScaleBytes));
+        const uint4* src = reinterpret_cast<const uint4*>(blk + (kv * S + slot) * (kD / 2) + 32 * l);
+        const uint8_t* sp = blk + S * kD + (kv * S + slot) * kScaleBytes;
+        uint32_t sb;
+        if constexpr (FP4) sb = __ldcg(reinterpret_cast<const uint32_t*>(sp) + l);
+        else sb = __ldcg(reinterpret_cast<const unsigned short*>(sp));
+        const uint4 a = __ldcg(src + l), b = __ldcg(src + (l ^ 1));  // slot t = chunk t ^ 4 l
+        const uint32_t cw[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if constexpr (FP4) {
+          row_fp4<BLOCK, BF16>(cw, l ? prmt(sb, sb, 0x1032u) : sb, p.cb, l, pmask, o);
+        } else {
+          const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sb)));
+          row_int4<BLOCK, BF16>(cw, BLOCK > 1 ? __fmul_rn(s, p.cb) : s, l, pmask, o);
+        }
+      }
+      const uint32_t dst = smem_addr(stage[w]) + (lane >> 1) * kRowStride + 128 * l;
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + 16 * (i ^ (4 * l))), "r"(o[4 * i]),
+                     "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                     : "memory");
     }
   }
-  uint8_t* dst = out + ((static_cast<size_t>(t) * p.num_kv_heads + h) * kD + 64 * l) * 2;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const uint32_t v[8] = {o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3],
-                           o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]};
-    stg_256(dst + 32 * i, v);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (have && l == 0) {
+    bulk_copy_s2g(out + (static_cast<size_t>(t) * p.num_kv_heads + h) * (2 * kD),
+                  smem_addr(stage[w]) + (lane >> 1) * kRowStride, 2 * kD);
+    bulk_commit();
+    bulk_wait_read();  // the copy reads this CTA's memory: stay until it has
   }
 }
 
