@@ -9,8 +9,8 @@
 // NVFP4: the stages inside a block of 16 channels are exact in fp16 as well (|sum| <= 6 * 16
 // in steps of 1/2); the scales and the stages across blocks are fp32.
 //
-// Layout.  A warp takes the K or the V rows of 16 consecutive tokens of one KV head (1 KB of
-// codes, contiguous inside a page); two lanes hold a row, lane l the channels [64 l, 64 l + 64),
+// Layout.  A warp takes the K and the V rows of 16 consecutive tokens of one KV head (1 KB of
+// codes each, contiguous inside a page, all in flight at once); two lanes hold a row, lane l the channels [64 l, 64 l + 64),
 // so that only b = 128 exchanges data between lanes.  The finished rows go through shared memory
 // and leave by one bulk copy each: stored from registers, a lane's 128 bytes are a line of their
 // own in every store and the L1 data path takes 32 passes per kilobyte.  Slot t of lane l holds
@@ -206,19 +206,16 @@ __device__ __forceinline__ void row_fp4(const uint32_t (&w)[8], uint32_t sc, flo
 
 template <int BLOCK, bool FP4, bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) gather_kernel(GatherParams p) {
-  __shared__ __align__(128) uint8_t stage[kWarps][kRowsPerWarp * kRowStride];
+  __shared__ __align__(128) uint8_t stage[kWarps][2][kRowsPerWarp * kRowStride];
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, l = lane & 1;
   const unsigned pmask = 0x3u << (lane & 30);
-  // Item: (16 tokens, head, K or V), K or V fastest, then the head.
+  // Item: (16 tokens, head), the head fastest.
   const int item = blockIdx.x * kWarps + w;
-  const int per_group = 2 * p.num_kv_heads;
-  const int tg = item / per_group, rest = item - tg * per_group;
-  const int h = rest >> 1, kv = rest & 1;
+  const int tg = item / p.num_kv_heads, h = item - tg * p.num_kv_heads;
   const int t = tg * kRowsPerWarp + (lane >> 1);
-  uint8_t* const out = static_cast<uint8_t*>(kv ? p.v_out : p.k_out);
-  bool have = out != nullptr && t < p.total_rows;  // (the same in both lanes of a row)
+  bool have = t < p.total_rows;  // (the same in both lanes of a row)
   if (have) {
     int lo = 0, hi = p.batch;
     while (hi - lo > 1) {
@@ -232,46 +229,59 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(GatherParams p) {
       int page = -1;
       const bool bad_pos = pos < 0 || (pos >> p.page_shift) >= p.max_pages_per_seq;
       if (!bad_pos) page = __ldg(p.page_table + static_cast<size_t>(lo) * p.max_pages_per_seq + (pos >> p.page_shift));
-      uint32_t o[32];
-      if (page < 0 || page >= p.num_pages) {
-        atomicOr(p.status, bad_pos ? KVQ_DEV_BAD_POS_BIT : KVQ_DEV_BAD_PAGE_BIT);
+      const bool good = page >= 0 && page < p.num_pages;
+      if (!good) atomicOr(p.status, bad_pos ? KVQ_DEV_BAD_POS_BIT : KVQ_DEV_BAD_PAGE_BIT);
+      // Both rows' codes and scales (zeros for a bad page), in flight together.
+      constexpr int kScaleBytes = FP4 ? kD / 16 : 2;
+      uint4 ca[2], cb[2];
+      uint32_t sb[2] = {0u, 0u};
 #pragma unroll
-        for (int i = 0; i < 32; i++) o[i] = 0u;
-      } else {
-        constexpr int kScaleBytes = FP4 ? kD / 16 : 2;
+      for (int kv = 0; kv < 2; kv++) ca[kv] = cb[kv] = make_uint4(0u, 0u, 0u, 0u);
+      if (good) {
         const int S = p.page_size, slot = static_cast<int>(pos) & (S - 1);
         const uint8_t* blk = p.pool_layer + (static_cast<size_t>(page) * p.num_kv_heads + h) *
                                                 (static_cast<size_t>(S) * (kD + 2 * kScaleBytes));
-        const uint4* src = reinterpret_cast<const uint4*>(blk + (kv * S + slot) * (kD / 2) + 32 * l);
-        const uint8_t* sp = blk + S * kD + (kv * S + slot) * kScaleBytes;
-        uint32_t sb;
-        if constexpr (FP4) sb = __ldcg(reinterpret_cast<const uint32_t*>(sp) + l);
-        else sb = __ldcg(reinterpret_cast<const unsigned short*>(sp));
-        const uint4 a = __ldcg(src + l), b = __ldcg(src + (l ^ 1));  // slot t = chunk t ^ 4 l
-        const uint32_t cw[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        if constexpr (FP4) {
-          row_fp4<BLOCK, BF16>(cw, l ? prmt(sb, sb, 0x1032u) : sb, p.cb, l, pmask, o);
-        } else {
-          const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sb)));
-          row_int4<BLOCK, BF16>(cw, BLOCK > 1 ? __fmul_rn(s, p.cb) : s, l, pmask, o);
+#pragma unroll
+        for (int kv = 0; kv < 2; kv++) {
+          if (!(kv ? p.v_out : p.k_out)) continue;
+          const uint4* src = reinterpret_cast<const uint4*>(blk + (kv * S + slot) * (kD / 2) + 32 * l);
+          const uint8_t* sp = blk + S * kD + (kv * S + slot) * kScaleBytes;
+          ca[kv] = __ldcg(src + l);  // slot t = chunk t ^ 4 l
+          cb[kv] = __ldcg(src + (l ^ 1));
+          if constexpr (FP4) sb[kv] = __ldcg(reinterpret_cast<const uint32_t*>(sp) + l);
+          else sb[kv] = __ldcg(reinterpret_cast<const unsigned short*>(sp));
         }
       }
-      const uint32_t dst = smem_addr(stage[w]) + (lane >> 1) * kRowStride + 128 * l;
 #pragma unroll
-      for (int i = 0; i < 8; i++)
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + 16 * (i ^ (4 * l))), "r"(o[4 * i]),
-                     "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
-                     : "memory");
+      for (int kv = 0; kv < 2; kv++) {
+        if (!(kv ? p.v_out : p.k_out)) continue;
+        const uint32_t cw[8] = {ca[kv].x, ca[kv].y, ca[kv].z, ca[kv].w, cb[kv].x, cb[kv].y, cb[kv].z, cb[kv].w};
+        uint32_t o[32];
+        if constexpr (FP4) {
+          row_fp4<BLOCK, BF16>(cw, l ? prmt(sb[kv], sb[kv], 0x1032u) : sb[kv], p.cb, l, pmask, o);
+        } else {
+          const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sb[kv])));
+          row_int4<BLOCK, BF16>(cw, BLOCK > 1 ? __fmul_rn(s, p.cb) : s, l, pmask, o);
+        }
+        const uint32_t dst = smem_addr(stage[w][kv]) + (lane >> 1) * kRowStride + 128 * l;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + 16 * (i ^ (4 * l))), "r"(o[4 * i]),
+                       "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                       : "memory");
+        // The row leaves when both of its lanes have stored.
+        fence_proxy_async_smem();
+        __syncwarp(pmask);
+        if (l == 0) {
+          uint8_t* const out = static_cast<uint8_t*>(kv ? p.v_out : p.k_out);
+          bulk_copy_s2g(out + (static_cast<size_t>(t) * p.num_kv_heads + h) * (2 * kD),
+                        smem_addr(stage[w][kv]) + (lane >> 1) * kRowStride, 2 * kD);
+          bulk_commit();
+        }
+      }
     }
   }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (have && l == 0) {
-    bulk_copy_s2g(out + (static_cast<size_t>(t) * p.num_kv_heads + h) * (2 * kD),
-                  smem_addr(stage[w]) + (lane >> 1) * kRowStride, 2 * kD);
-    bulk_commit();
-    bulk_wait_read();  // the copy reads this CTA's memory: stay until it has
-  }
+  if (have && l == 0) bulk_wait_read();  // the copies read this CTA's memory: stay until they have
 }
 
 template <int BLOCK, bool FP4>
@@ -295,11 +305,10 @@ int launch_block(const cudaLaunchConfig_t& cfg, const GatherParams& p, int block
 
 }  // namespace
 
-int launch_gather(const GatherParams& p, int block, bool fp4, bool bf16, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
+int launch_gather(const GatherParams& p, int block, bool fp4, bool bf16, cudaStream_t stream) {
   if (p.total_rows == 0) return 0;
   const long long items =
-      (static_cast<long long>(p.total_rows) + kRowsPerWarp - 1) / kRowsPerWarp * 2 * p.num_kv_heads;
+      (static_cast<long long>(p.total_rows) + kRowsPerWarp - 1) / kRowsPerWarp * p.num_kv_heads;
   if (items > 0x7fffffffLL - kWarps) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps));

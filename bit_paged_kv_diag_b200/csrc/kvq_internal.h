@@ -230,7 +230,7 @@ struct SparseParams {
 // Host-side launchers of the position-rotating append, the read-back, and block-sparse
 // attention with its bounds and selection.
 int launch_rope_append(RopeAppendParams p, int block, bool fp4, bool bf16, int num_sms, cudaStream_t stream);
-int launch_gather(const GatherParams& p, int block, bool fp4, bool bf16, int num_sms, cudaStream_t stream);
+int launch_gather(const GatherParams& p, int block, bool fp4, bool bf16, cudaStream_t stream);
 int launch_bounds(const BoundsParams& p, bool fp4, cudaStream_t stream);
 int launch_select(SelectParams p, int num_sms, cudaStream_t stream);
 

@@ -118,7 +118,7 @@ int kvq_gather_rows(kvq_cache* c, int32_t layer, const int32_t* cu_rows, const i
   p.page_shift = shift_of(c);
   p.max_pages_per_seq = c->d.max_pages_per_seq;
   p.cb = c->cb;
-  return status_of(kvq::launch_gather(p, c->d.hadamard_block, fp4_of(c), dtype == KVQ_DTYPE_BF16, c->num_sms,
+  return status_of(kvq::launch_gather(p, c->d.hadamard_block, fp4_of(c), dtype == KVQ_DTYPE_BF16,
                                       static_cast<cudaStream_t>(stream)));
 }
 
