@@ -10,7 +10,7 @@
 //
 // Work split.  A unit is (query, KV head) and has ceil(num_blocks * S / 32) tiles of 32 tokens.
 // A CTA of 4 warps takes one of `splits` equal parts of a unit; its warps take the part's tiles
-// in turn through their own rings of 3 shared-memory slots (bulk copies, one per page and piece)
+// in turn through their own rings of shared-memory slots (bulk copies, one per page and piece)
 // and merge in shared memory.  Tiles without a token to attend are skipped before their copy.
 // With splits > 1 (few units: the parts fill the SMs), each CTA leaves one record per query head
 // in the handle's scratch and the last to arrive merges them in the order of the parts, so the
@@ -28,6 +28,10 @@ namespace kvq {
 namespace {
 
 constexpr int kMaxSplits = 8;
+constexpr int kCtasPerSm = 4;
+// Ring slots of a warp: four CTAs of either format fit into an SM's shared memory.
+template <bool FP4>
+constexpr int kRing = FP4 ? 2 : 3;
 
 // A page of a tile, one per lane: its block's address (16-byte aligned; bits 0-2 = the tile's
 // first token in the page / 32), and the tokens to attend in the tile's part of it (<= 0: none).
@@ -107,26 +111,26 @@ __device__ __forceinline__ void issue_tile(Entry e, uint32_t slot, uint32_t bar,
 }
 
 template <int G, int SEFF, bool FP4>
-__global__ void __launch_bounds__(kThreads, 3) sparse_kernel(DecodeParams p, SparseParams sp, int splits) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodeParams p, SparseParams sp, int splits) {
   constexpr int kSlot = slot_bytes(FP4);
   constexpr int kPPT = Tiles<SEFF>::kPPT, kBatch = Tiles<SEFF>::kBatch;
   griddep_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
   uint8_t* ring = smem;                                                        // [w][stage][kSlot]
-  uint8_t* qraw = ring + kWarps * kStages * kSlot;                             // [G][128] fp16
+  uint8_t* qraw = ring + kWarps * kRing<FP4> * kSlot;                             // [G][128] fp16
   uint32_t* frag = reinterpret_cast<uint32_t*>(qraw + G * kD * 2);             // [frag_words]
   float* sf = reinterpret_cast<float*>(frag + frag_words(G, FP4));             // [8]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sf + 8);                        // [w][kStages]
-  __shared__ int2 valid_ring[kWarps][kStages];  // tokens to attend of the tile in each slot
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sf + 8);                        // [w][kRing<FP4>]
+  __shared__ int2 valid_ring[kWarps][kRing<FP4>];  // tokens to attend of the tile in each slot
   __shared__ int last_flag;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int unit = blockIdx.x / splits, part = blockIdx.x - unit * splits;
   const int t = unit / p.num_kv_heads, h = unit - t * p.num_kv_heads;
-  const uint32_t bar_s = smem_addr(bars + w * kStages);
+  const uint32_t bar_s = smem_addr(bars + w * kRing<FP4>);
   if (lane == 0) {
 #pragma unroll
-    for (int s = 0; s < kStages; s++) mbar_init(bar_s + 8 * s, 1);
+    for (int s = 0; s < kRing<FP4>; s++) mbar_init(bar_s + 8 * s, 1);
     fence_mbar_init();
   }
   __syncwarp();
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_kernel(DecodeParams p, Spa
   const int x0 = static_cast<int>(static_cast<long long>(ntile) * part / splits);
   const int x1 = static_cast<int>(static_cast<long long>(ntile) * (part + 1) / splits);
   const int nT = max(0, (x1 - x0 - w + kWarps - 1) / kWarps);
-  uint8_t* const ring_w = ring + w * kStages * kSlot;
+  uint8_t* const ring_w = ring + w * kRing<FP4> * kSlot;
   const uint32_t ring_s = smem_addr(ring_w);
   // Producer: batches of kBatch tiles; `todo` holds the batch's tiles that have a token.
   int tb = -kBatch;
@@ -188,12 +192,12 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_kernel(DecodeParams p, Spa
     e.addr = __shfl_sync(kFull, cur.addr, (i + lane) & 31);
     e.ntok = __shfl_sync(kFull, cur.ntok, (i + lane) & 31);
     const int n0 = __shfl_sync(kFull, e.ntok, 0), n1 = __shfl_sync(kFull, e.ntok, 1);
-    const int s = issued % kStages;
+    const int s = issued % kRing<FP4>;
     if (lane == 0) valid_ring[w][s] = kPPT == 2 ? make_int2(n0, n1) : make_int2(n0, n0 - 16);
     issue_tile<SEFF, FP4>(e, ring_s + s * kSlot, bar_s + 8 * s, lane, p);
     issued++;
   };
-  for (int i = 0; i < kStages; i++) produce();
+  for (int i = 0; i < kRing<FP4>; i++) produce();
 
   // q of the unit: rotated and cut by all warps.
   {
@@ -228,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_kernel(DecodeParams p, Spa
   // As in the decode kernel: the scores and statistics of the next tile next to the PV of the
   // current one.
   while (consumed + 1 < issued && !dead) {
-    const int cs = slot_i, ns = cs + 1 == kStages ? 0 : cs + 1;
-    const uint32_t npar = cs + 1 == kStages ? parity ^ 1u : parity;
+    const int cs = slot_i, ns = cs + 1 == kRing<FP4> ? 0 : cs + 1;
+    const uint32_t npar = cs + 1 == kRing<FP4> ? parity ^ 1u : parity;
     if (!mbar_wait_bounded(bar_s + 8 * ns, npar, kWaitLimitNs)) {
       dead = true;
       break;
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_kernel(DecodeParams p, Spa
     // Flag it and let the copies still in flight land (bounded) before their memory is reused.
     if (lane == 0) atomicOr(p.status, KVQ_DEV_TIMEOUT_BIT);
     for (int j = consumed; j < issued; j++)
-      mbar_wait_bounded(bar_s + 8 * (j % kStages), static_cast<uint32_t>((j / kStages) & 1), kWaitLimitNs);
+      mbar_wait_bounded(bar_s + 8 * (j % kRing<FP4>), static_cast<uint32_t>((j / kRing<FP4>) & 1), kWaitLimitNs);
   }
   // The warps' records, each in its own drained ring; an idle warp's has m = -inf, l = 0.
   __syncwarp();
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_kernel(DecodeParams p, Spa
   state_write<G>(st, rec_w, lane);
   __syncthreads();
   __half* const orow = p.out + (static_cast<size_t>(t) * p.num_kv_heads + h) * G * kD;
-  auto rec = [&](int j) -> const float* { return reinterpret_cast<const float*>(ring) + j * (kStages * kSlot / 4); };
+  auto rec = [&](int j) -> const float* { return reinterpret_cast<const float*>(ring) + j * (kRing<FP4> * kSlot / 4); };
   auto part_rec = [&](int j) { return p.part + (static_cast<size_t>(unit) * splits + j) * G * kPartStride; };
   merge_few<G, kWarps, false, kWarps>(kWarps, rec, w, orow, splits > 1 ? part_rec(part) : nullptr, lane, p);
   if (splits == 1) return;
@@ -285,9 +289,9 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_kernel(DecodeParams p, Spa
 }
 
 size_t smem_bytes(int group, bool fp4) {
-  size_t s = static_cast<size_t>(kWarps) * kStages * slot_bytes(fp4);
+  size_t s = static_cast<size_t>(kWarps) * (fp4 ? kRing<true> : kRing<false>) * slot_bytes(fp4);
   s += static_cast<size_t>(group) * kD * 2 + sizeof(uint32_t) * frag_words(group, fp4) + 8 * sizeof(float);
-  s += sizeof(uint64_t) * kWarps * kStages + 128;
+  s += sizeof(uint64_t) * kWarps * 4 + 128;
   return (s + 15) & ~static_cast<size_t>(15);
 }
 
@@ -309,12 +313,12 @@ int launch_group(const cudaLaunchConfig_t& cfg, const DecodeParams& p, const Spa
 int launch_sparse(const DecodeParams& p, const SparseParams& sp, int num_sms, cudaStream_t stream) {
   const long long units = static_cast<long long>(sp.total_q) * p.num_kv_heads;
   if (units == 0) return 0;
-  // Parts of a unit: as many as fill the SMs' three CTAs each, while every warp keeps a tile and
+  // Parts of a unit: as many as fill the SMs' CTAs, while every warp keeps a tile and
   // the scratch has a record and a counter for each.
   const int ntile = static_cast<int>((static_cast<long long>(sp.num_blocks) * p.page_size + kTileTokens - 1) / kTileTokens);
   int splits = 1;
   if (units <= sp.num_counters) {
-    const long long fit = 3LL * num_sms / units, slots = sp.num_slots / units, work = (ntile + kWarps - 1) / kWarps;
+    const long long fit = static_cast<long long>(kCtasPerSm) * num_sms / units, slots = sp.num_slots / units, work = (ntile + kWarps - 1) / kWarps;
     long long s = fit < kMaxSplits ? fit : kMaxSplits;
     if (s > slots) s = slots;
     if (s > work) s = work;
