@@ -71,6 +71,7 @@ class Desc(ctypes.Structure):
 
 
 _lib = None
+_torch = None  # the torch module, imported with the first cache
 
 
 def lib() -> ctypes.CDLL:
@@ -172,6 +173,8 @@ class Cache:
     when the caller supplied one (kept alive here)."""
 
     def __init__(self, handle, desc, pool_tensor, device=None):
+        global _torch
+        import torch as _torch
         self.handle = handle
         self.desc = desc
         self.pool = pool_tensor
@@ -180,7 +183,7 @@ class Cache:
         self.kv_heads, self.q_heads = desc.num_kv_heads, desc.num_q_heads
         self.table_width = desc.max_pages_per_seq
         self.page_shape = (desc.num_layers, desc.num_pages, desc.num_kv_heads)
-        self.torch_device = None if device is None else f"cuda:{device}"
+        self.torch_device = None if device is None else _torch.device("cuda", device)
 
     @property
     def pool_ptr(self) -> int:
@@ -347,10 +350,9 @@ class BlockBounds:
                    torch.zeros(*shape, dtype=torch.float32, device=dev))
 
     def pointers(self, cache):
-        import torch
         shape = cache.page_shape
-        return (_arg(cache, self.codes, "codes", torch.int8, (*shape, 2, 128)),
-                _arg(cache, self.scale, "scale", torch.float32, shape))
+        return (_arg(cache, self.codes, "codes", _torch.int8, (*shape, 2, 128)),
+                _arg(cache, self.scale, "scale", _torch.float32, shape))
 
 
 def _arg(cache, t, what, dtype, shape):
@@ -372,8 +374,7 @@ def _refuse(cache, t, what, shape):
 
 def _seqs(cache, seq_lens, page_table, cu, cu_name):
     """(batch, pointers of seq_lens, page_table and cu) of a call, checked."""
-    import torch
-    i32, batch = torch.int32, seq_lens.shape[0]
+    i32, batch = _torch.int32, seq_lens.shape[0]
     return (batch, _arg(cache, seq_lens, "seq_lens", i32, (batch,)),
             _arg(cache, page_table, "page_table", i32, (batch, cache.table_width)),
             None if cu is None else _arg(cache, cu, cu_name, i32, (batch + 1,)))
@@ -381,16 +382,15 @@ def _seqs(cache, seq_lens, page_table, cu, cu_name):
 
 def _run(cache, stream, name, *args):
     """Call the library on the cache's device and the given (default: current) stream."""
-    import torch
     fn = getattr(_lib, name)
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(cache.device)
+        stream = _torch._C._cuda_getCurrentRawStream(cache.device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == cache.device:
+    if _torch._C._cuda_getDevice() == cache.device:
         rc = fn(cache.handle, *args, stream)
     else:
-        with torch.cuda.device(cache.device):
+        with _torch.cuda.device(cache.device):
             rc = fn(cache.handle, *args, stream)
     if rc != KVQ_OK:
         raise KVQError(name, rc)
@@ -398,13 +398,12 @@ def _run(cache, stream, name, *args):
 
 def _empty(cache, shape, dtype, stream):
     """An output of the call's stream (so that the allocator orders its reuse after the call)."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=cache.torch_device)
+        return _torch.empty(shape, dtype=dtype, device=cache.torch_device)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=cache.torch_device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=cache.torch_device)
+        stream = _torch.cuda.ExternalStream(stream, device=cache.torch_device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=cache.torch_device)
 
 
 def _tokens(cache, t, what, dtype, shape):
@@ -425,10 +424,9 @@ def _tokens(cache, t, what, dtype, shape):
 
 
 def _dtype_code(dtype):
-    import torch
-    if dtype == torch.float16:
+    if dtype == _torch.float16:
         return 0
-    if dtype == torch.bfloat16:
+    if dtype == _torch.bfloat16:
         return 1
     raise TypeError(f"rows must be float16 or bfloat16, got {dtype}")
 
@@ -439,21 +437,20 @@ def rope_quant_append(cache: Cache, layer: int, k, v, cu_new_tokens, seq_lens, p
     k, v [T][Hkv][128] and q [T][Hq][128], all fp16 or all bf16, may be slices of one qkv buffer
     (a token's heads contiguous, any token stride).  Angles use the cache positions, or
     ``positions`` int32 [T].  Returns the rotated q in fp16 [T][Hq][128] (None without q)."""
-    import torch
     T, dtype = k.shape[0], k.dtype
     code = _dtype_code(dtype)
     kp, ks = _tokens(cache, k, "k", dtype, (T, cache.kv_heads, 128))
     vp, vs = _tokens(cache, v, "v", dtype, (T, cache.kv_heads, 128))
     batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_new_tokens, "cu_new_tokens")
-    pos = None if positions is None else _arg(cache, positions, "positions", torch.int32, (T,))
-    freq = _arg(cache, rope.inv_freq, "inv_freq", torch.float32, (rope.rotary_dim // 2,))
+    pos = None if positions is None else _arg(cache, positions, "positions", _torch.int32, (T,))
+    freq = _arg(cache, rope.inv_freq, "inv_freq", _torch.float32, (rope.rotary_dim // 2,))
     qp, qs, op = None, 0, None
     if q is not None:
         shape = (T, cache.q_heads, 128)
         qp, qs = _tokens(cache, q, "q", dtype, shape)
         if q_out is None:
-            q_out = _empty(cache, shape, torch.float16, stream)
-        op = _arg(cache, q_out, "q_out", torch.float16, shape)
+            q_out = _empty(cache, shape, _torch.float16, stream)
+        op = _arg(cache, q_out, "q_out", _torch.float16, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
     _run(cache, stream, "kvq_rope_quant_append", int(layer), code, qp, qs, kp, ks, vp, vs, cu, sl, pos, pt,
@@ -466,8 +463,7 @@ def gather_rows(cache: Cache, layer: int, cu_rows, starts, page_table, total_row
     """Cached K and V rows in the model's basis: positions starts[b] .. starts[b] + cu_rows[b+1] -
     cu_rows[b] - 1 of every sequence, as two tensors [total_rows][Hkv][128] of ``dtype`` (fp16
     unless given; bf16)."""
-    import torch
-    dtype = torch.float16 if dtype is None else dtype
+    dtype = _torch.float16 if dtype is None else dtype
     code = _dtype_code(dtype)
     shape = (int(total_rows), cache.kv_heads, 128)
     batch, st, pt, cu = _seqs(cache, starts, page_table, cu_rows, "cu_rows")
@@ -496,14 +492,13 @@ def select_blocks(cache: Cache, layer: int, q, seq_lens, page_table, bounds: Blo
     others by the bounds' score; int32 [total_q][Hkv][num_blocks], ascending, then -1.  q fp16
     [total_q][Hq][128]; one query per sequence, or the chunks of ``cu_q``.  seq_lens counts the
     queries' own tokens."""
-    import torch
     tq, nb = q.shape[0], int(num_blocks)
     batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_q, "cu_q")
     codes, scale = bounds.pointers(cache)
-    qp = _arg(cache, q, "q", torch.float16, (tq, cache.q_heads, 128))
+    qp = _arg(cache, q, "q", _torch.float16, (tq, cache.q_heads, 128))
     if blocks is None:
-        blocks = _empty(cache, (tq, cache.kv_heads, max(nb, 0)), torch.int32, stream)
-    bp = _arg(cache, blocks, "blocks", torch.int32, (tq, cache.kv_heads, max(nb, 0)))
+        blocks = _empty(cache, (tq, cache.kv_heads, max(nb, 0)), _torch.int32, stream)
+    bp = _arg(cache, blocks, "blocks", _torch.int32, (tq, cache.kv_heads, max(nb, 0)))
     _run(cache, stream, "kvq_select_blocks", int(layer), codes, scale, qp, cu, sl, pt, batch, tq, nb,
          int(sink), int(recent), bp)
     return blocks
@@ -514,17 +509,16 @@ def sparse_attention(cache: Cache, layer: int, q, seq_lens, page_table, blocks, 
     """Attention of every query over the pages in its own list: blocks int32
     [total_q][Hkv][num_blocks] (negative: empty), as :func:`select_blocks` returns it or the
     caller's own; q, seq_lens, cu_q as there.  Returns fp16 [total_q][Hq][128]."""
-    import torch
     tq = q.shape[0]
     batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_q, "cu_q")
-    qp = _arg(cache, q, "q", torch.float16, (tq, cache.q_heads, 128))
+    qp = _arg(cache, q, "q", _torch.float16, (tq, cache.q_heads, 128))
     if blocks.dim() != 3:
         raise ValueError("blocks must be [total_q][num_kv_heads][num_blocks]")
     nb = int(blocks.shape[2])
-    bp = _arg(cache, blocks, "blocks", torch.int32, (tq, cache.kv_heads, nb))
+    bp = _arg(cache, blocks, "blocks", _torch.int32, (tq, cache.kv_heads, nb))
     if out is None:
-        out = _empty(cache, (tq, cache.q_heads, 128), torch.float16, stream)
-    op = _arg(cache, out, "out", torch.float16, (tq, cache.q_heads, 128))
+        out = _torch.empty_like(q) if stream is None else _empty(cache, (tq, cache.q_heads, 128), _torch.float16, stream)
+    op = _arg(cache, out, "out", _torch.float16, (tq, cache.q_heads, 128))
     _run(cache, stream, "kvq_sparse_attention", int(layer), qp, cu, sl, pt, bp, nb, batch, tq,
          float(softmax_scale), op)
     return out

@@ -80,11 +80,7 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(BoundsParams p) {
   // Item slots: sequence b has those from cu[b] / S + 2 b on, at least as many as the pages that
   // its tokens can touch ((n - 1) / S + 2), so an item finds its sequence without a prefix sum.
   auto slot0 = [&](int b) { return (__ldg(p.cu_new_tokens + b) >> p.page_shift) + 2 * b; };
-  int lo = 0, hi = p.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (slot0(mid) <= item) lo = mid; else hi = mid;
-  }
+  const int lo = warp_find(p.batch, item, slot0);
   const int n = __ldg(p.cu_new_tokens + lo + 1) - __ldg(p.cu_new_tokens + lo);
   const int j = item - slot0(lo);
   if (n <= 0 || j < 0) return;

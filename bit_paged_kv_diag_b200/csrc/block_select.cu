@@ -202,12 +202,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
   int b = item, t0 = item, nq = 1, n = 1, i0 = 0;
   if (p.cu_q) {
     auto slot0 = [&](int s) { return __ldg(p.cu_q + s) / Q + s; };
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (slot0(mid) <= item) lo = mid; else hi = mid;
-    }
-    b = lo;
+    b = warp_find(p.batch, item, slot0);
     const int first = __ldg(p.cu_q + b);
     n = __ldg(p.cu_q + b + 1) - first;
     i0 = (item - slot0(b)) * Q;

@@ -215,15 +215,12 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(GatherParams p) {
   const int item = blockIdx.x * kWarps + w;
   const int tg = item / p.num_kv_heads, h = item - tg * p.num_kv_heads;
   const int t = tg * kRowsPerWarp + (lane >> 1);
+  int first, next;
+  const SeqWindow win = seq_window(p.cu_rows, p.batch, tg * kRowsPerWarp);
+  const int lo = seq_find(win, p.cu_rows, p.batch, t, first, next);
   bool have = t < p.total_rows;  // (the same in both lanes of a row)
   if (have) {
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.cu_rows + mid) <= t) lo = mid; else hi = mid;
-    }
-    const int first = __ldg(p.cu_rows + lo);
-    have = t >= first && t < __ldg(p.cu_rows + lo + 1);  // otherwise a row of no sequence: left as it is
+    have = t >= first && t < next;  // otherwise a row of no sequence: left as it is
     if (have) {
       const long long pos = static_cast<long long>(__ldg(p.starts + lo)) + (t - first);
       int page = -1;

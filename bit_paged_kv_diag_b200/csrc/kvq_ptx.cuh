@@ -155,6 +155,57 @@ __device__ __forceinline__ void stg_128(void* p, uint32_t a, uint32_t b, uint32_
                : "memory");
 }
 
+// The last of the n entries f(0) <= f(1) <= ... that is <= x (entry 0 if none is), by a whole warp:
+// every round probes 32 places at once, so up to 32 entries cost one round trip and 1024 two (a
+// binary search costs one for each bit).
+template <typename F>
+__device__ __forceinline__ int warp_find(int n, int x, F&& f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const bool below = i < n && f(lo + i) <= x;
+    const int k = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+// Sequences of a run of tokens that starts at t0, by a whole warp: 32 neighbouring offsets of
+// cu[0 .. batch] held one per lane, so that every lane finds the sequence of its own token
+// t >= t0 by shuffles.
+struct SeqWindow {
+  int b0, offset;  // lane i: cu[min(b0 + i, batch)]
+};
+__device__ __forceinline__ SeqWindow seq_window(const int32_t* cu, int batch, int t0) {
+  SeqWindow s;
+  s.b0 = batch < 32 ? 0 : warp_find(batch, t0, [&](int i) { return __ldg(cu + i); });
+  s.offset = __ldg(cu + min(s.b0 + static_cast<int>(threadIdx.x & 31), batch));
+  return s;
+}
+// b = the last sequence below batch with cu[b] <= t; first, next = cu[b], cu[b + 1].
+__device__ __forceinline__ int seq_find(const SeqWindow& s, const int32_t* cu, int batch, int t, int& first,
+                                        int& next) {
+  int k = 0;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    if (__shfl_sync(0xffffffffu, s.offset, k + d) <= t && s.b0 + k + d < batch) k += d;
+  first = __shfl_sync(0xffffffffu, s.offset, k);
+  next = __shfl_sync(0xffffffffu, s.offset, min(k + 1, 31));
+  int b = s.b0 + k;
+  if (k == 31) {  // behind the window (empty sequences)
+    int hi = batch;
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (__ldg(cu + mid) <= t) b = mid; else hi = mid;
+    }
+    first = __ldg(cu + b);
+    next = __ldg(cu + b + 1);
+  }
+  return b;
+}
+
 // ------------------------------------------------------------ shared loads --
 __device__ __forceinline__ uint4 lds_128(uint32_t addr) {
   uint4 r;

@@ -40,7 +40,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStageRows = 16;        // rows of a warp stage: two lanes per row
 constexpr int kTileRows = 128;        // K and V rows of a CTA's tile, about 32 KB
-constexpr int kRopeTokens = 32;       // tokens of a tile at most
+constexpr int kRopeTokens = 32;       // tokens of a tile at most: a lane each
 constexpr int kMaxSmem = (kTileRows + 2 * 15) * kRow + kRopeTokens * (kD * 4 + 16) + 16;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bounded waits: 2 s
 
@@ -241,31 +241,30 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
     src += static_cast<int64_t>(t0 + t) * (kind ? p.v_stride : p.k_stride) * 2 + static_cast<int64_t>(h0) * kRow;
     bulk_copy_g2s((kind ? v_s : k_s) + t * nh * kRow, src, nh * kRow, bar, l2_policy_evict_first());
   }
-  // Each token's sequence, destination and position.
-  for (int i = tid; i < nt; i += kThreads) {
-    const int t = t0 + i;
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.cu_new_tokens + mid) <= t) lo = mid; else hi = mid;
-    }
-    const int first = __ldg(p.cu_new_tokens + lo);
-    TokenDest d = {-1, kSlotPadding, 0, 0};
-    if (t >= first && t < __ldg(p.cu_new_tokens + lo + 1)) {
-      const long long pos = static_cast<long long>(__ldg(p.seq_lens + lo)) + (t - first);
-      d.pos = p.positions ? __ldg(p.positions + t) : static_cast<int>(pos);
-      d.slot = kSlotBadPos;
-      if (pos >= 0 && (pos >> p.page_shift) < p.max_pages_per_seq) {
-        d.slot = static_cast<int>(pos) & (p.page_size - 1);
-        d.page = __ldg(p.page_table + static_cast<size_t>(lo) * p.max_pages_per_seq + (pos >> p.page_shift));
+  // Each token's sequence, destination and position: a lane per token.
+  if (w == 0) {
+    const int t = t0 + lane;
+    int first, next;
+    const SeqWindow win = seq_window(p.cu_new_tokens, p.batch, t0);
+    const int b = seq_find(win, p.cu_new_tokens, p.batch, t, first, next);
+    if (lane < nt) {
+      TokenDest d = {-1, kSlotPadding, 0, 0};
+      if (t >= first && t < next) {
+        const long long pos = static_cast<long long>(__ldg(p.seq_lens + b)) + (t - first);
+        d.pos = p.positions ? __ldg(p.positions + t) : static_cast<int>(pos);
+        d.slot = kSlotBadPos;
+        if (pos >= 0 && (pos >> p.page_shift) < p.max_pages_per_seq) {
+          d.slot = static_cast<int>(pos) & (p.page_size - 1);
+          d.page = __ldg(p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq + (pos >> p.page_shift));
+        }
+        if (d.slot < 0) atomicOr(p.status, KVQ_DEV_BAD_POS_BIT);
+        else if (d.page < 0 || d.page >= p.num_pages) {
+          atomicOr(p.status, KVQ_DEV_BAD_PAGE_BIT);
+          d.page = -1;
+        }
       }
-      if (d.slot < 0) atomicOr(p.status, KVQ_DEV_BAD_POS_BIT);
-      else if (d.page < 0 || d.page >= p.num_pages) {
-        atomicOr(p.status, KVQ_DEV_BAD_PAGE_BIT);
-        d.page = -1;
-      }
+      dest[lane] = d;
     }
-    dest[i] = d;
   }
   __syncthreads();
   const int pairs = p.rotary_dim >> 1;

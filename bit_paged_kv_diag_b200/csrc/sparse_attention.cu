@@ -139,14 +139,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
   // The query's sequence and position.
   int b = t, pos;
   if (sp.cu_q) {
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(sp.cu_q + mid) <= t) lo = mid; else hi = mid;
-    }
-    b = lo;
-    const int end = __ldg(sp.cu_q + b + 1);
-    if (t < __ldg(sp.cu_q + b) || t >= end) return;  // a row of no sequence: left as it is
+    int first, end;
+    const SeqWindow win = seq_window(sp.cu_q, p.batch, t);
+    b = seq_find(win, sp.cu_q, p.batch, t, first, end);
+    if (t < first || t >= end) return;  // a row of no sequence: left as it is
     pos = __ldg(p.seq_lens + b) - (end - t);
   } else {
     pos = __ldg(p.seq_lens + b) - 1;
