@@ -32,8 +32,6 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "kvq_internal.h"
 #include "kvq_ptx.cuh"
 
@@ -228,7 +226,25 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
     const int g = lane >> 2, c = lane & 3;
     const int ntile = (nmax + kTilePages - 1) / kTilePages, step = kWarps * static_cast<int>(C);
     const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
-    // The first tile's rows are in flight while q is prepared.
+    const __half* qt = p.q + (static_cast<size_t>(t0) * p.num_kv_heads + h) * G * kD;
+    // Row i of the MMA tiles: heads 2 x and 2 x + 1 of a query in rows R and R + 8 (G = 1: a query
+    // each).
+    constexpr int kPairs = G > 1 ? G / 2 : 1;
+    auto query_of = [&](int i) { return G == 1 ? i : (i >> 4) * (16 / G) + (i & 7) / kPairs; };
+    auto load_q = [&](auto& raw, int i0) {
+#pragma unroll
+      for (int z = 0; z < static_cast<int>(sizeof(raw) / sizeof(raw[0])); z++) {
+        const int i = i0 + z * kWarps, q = query_of(i);
+        const int head = G == 1 ? 0 : 2 * ((i & 7) % kPairs) + ((i >> 3) & 1);
+        raw[z] = make_uint2(0u, 0u);
+        if (i < nrow && q < nq)
+          raw[z] = __ldcg(reinterpret_cast<const uint2*>(qt + (static_cast<size_t>(q) * p.num_kv_heads * G + head) * kD) + lane);
+      }
+    };
+    // A small tile's q rows are in flight first of all, then the first step's page rows.
+    const bool small = nrow <= 2 * kWarps;
+    uint2 raw2[2];
+    if (small) load_q(raw2, w);
     constexpr int kN = kTilePages / 8;
     u32x8 rows[kN][2];
     float sigma[kN];  // of page g of MMA tile r (0: no page there, or a bad one)
@@ -257,27 +273,15 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
     if (mt < ntile) load_rows(mt);
     load_ids(mt + step);
 
-    const __half* qt = p.q + (static_cast<size_t>(t0) * p.num_kv_heads + h) * G * kD;
-    // Row i of the MMA tiles: heads 2 x and 2 x + 1 of a query in rows R and R + 8 (G = 1: a query
-    // each).
-    constexpr int kPairs = G > 1 ? G / 2 : 1;
-    auto query_of = [&](int i) { return G == 1 ? i : (i >> 4) * (16 / G) + (i & 7) / kPairs; };
-    auto prep = [&](auto batch, int i0) {
-      constexpr int kBatch = decltype(batch)::value;
-      uint2 raw[kBatch];
-#pragma unroll
-      for (int z = 0; z < kBatch; z++) {
-        const int i = i0 + z * kWarps, q = query_of(i);
-        const int head = G == 1 ? 0 : 2 * ((i & 7) % kPairs) + ((i >> 3) & 1);
-        raw[z] = make_uint2(0u, 0u);
-        if (i < nrow && q < nq)
-          raw[z] = __ldcg(reinterpret_cast<const uint2*>(qt + (static_cast<size_t>(q) * p.num_kv_heads * G + head) * kD) + lane);
+    if (small) {
+      prep_rows<2>(raw2, frag, sq, w, nrow, lane, p);
+    } else {
+      for (int i0 = w; i0 < nrow; i0 += 4 * kWarps) {
+        uint2 raw[4];
+        load_q(raw, i0);
+        prep_rows<4>(raw, frag, sq, i0, nrow, lane, p);
       }
-      prep_rows<kBatch>(raw, frag, sq, i0, nrow, lane, p);
-    };
-    if (nrow <= 2 * kWarps) prep(std::integral_constant<int, 2>{}, w);
-    else
-      for (int i0 = w; i0 < nrow; i0 += 4 * kWarps) prep(std::integral_constant<int, 4>{}, i0);
+    }
     // Keys past the last scored tile of pages count for nothing.
     if (rank == 0) {
       const int from = ntile * kTilePages, to = key_words(nmax);
