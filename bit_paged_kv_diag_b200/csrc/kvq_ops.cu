@@ -101,7 +101,7 @@ int kvq_gather_rows(kvq_cache* c, int32_t layer, const int32_t* cu_rows, const i
   if (dtype != KVQ_DTYPE_FP16 && dtype != KVQ_DTYPE_BF16) return KVQ_EINVAL;
   if (total_rows == 0) return KVQ_OK;
   if (batch == 0 || !cu_rows || !starts || !page_table || (!k_out && !v_out)) return KVQ_EINVAL;
-  if (!aligned(k_out, 32) || !aligned(v_out, 32)) return KVQ_EINVAL;  // 256-bit stores
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return KVQ_EINVAL;  // bulk copies
   kvq::GatherParams p = {};
   p.pool_layer = layer_of(c, layer);
   p.cu_rows = cu_rows;

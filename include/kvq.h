@@ -76,7 +76,9 @@
  *     when the previous kernel on the stream lets its dependents start.  Kernels that do
  *     not use programmatic launch (PyTorch's, cuBLAS's, copies) only do so by completing,
  *     and this library's own kernels never write these arrays.  The calls from
- *     kvq_rope_quant_append to kvq_sparse_attention wait before they read anything.
+ *     kvq_rope_quant_append to kvq_sparse_attention wait before they read anything, and
+ *     kvq_gather_rows, whose outputs may be an append's k and v, completes before the next
+ *     kernel starts.
  *   * The current device must be the one the handle was made on; the calls from
  *     kvq_rope_quant_append to kvq_sparse_attention return KVQ_EINVAL otherwise.
  */
@@ -304,7 +306,7 @@ KVQ_API int kvq_rope_quant_append(kvq_cache* c, int32_t layer, int32_t dtype, co
  *   starts         device int32 [batch], first position read of each sequence
  *   total_rows     host int32, rows of the outputs
  *   dtype          KVQ_DTYPE_FP16 or KVQ_DTYPE_BF16, of the outputs
- *   k_out, v_out   device [total_rows][num_kv_heads][128], 32-byte aligned; either may be
+ *   k_out, v_out   device [total_rows][num_kv_heads][128], 16-byte aligned; either may be
  *                  NULL (that half is not read)
  * Rows behind cu_rows[batch] are left as they were; rows of a bad page or position are flagged
  * and zeros.  (An INT4 value outside fp16's range becomes infinite in fp16; bf16 holds it.) */

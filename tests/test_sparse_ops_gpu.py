@@ -177,6 +177,25 @@ def test_rope_append_without_angles_is_the_plain_append(fmt, block, page):
     assert torch.equal(a.pool, b.pool) and a.status() == 0
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_rope_append_large_and_zero_rows(fmt):
+    """bf16 rows beyond the scales' range (they saturate), tiny ones and zeros."""
+    s = Setup([3], [40], 2, 2, 64, 16, fmt)
+    torch = s.torch
+    x = s.rng.standard_normal((40, 2, D)).astype(np.float32)
+    x *= (10.0 ** s.rng.integers(-30, 30, (40, 2, 1))).astype(np.float32)
+    x[7] = 0
+    k = torch.from_numpy(x).bfloat16()
+    s.kvq.rope_quant_append(s.cache, 0, k.cuda(), k.cuda(), s.dev(s.cu), s.dev(s.before), s.pt,
+                            s.kvq.Rope(torch.ones(64, device="cuda")),
+                            positions=torch.zeros(40, dtype=torch.int32, device="cuda"))
+    c, sc = ref.quantise(ref.butterfly32(k.float().numpy(), 64), fmt)
+    P = s.host()
+    pg, sl = s.table[0, s.pos // 16], s.pos % 16
+    for kv in range(2):
+        assert np.array_equal(P.parts[2 + kv][pg, :, sl], sc) and np.array_equal(P.codes(kv)[pg, :, sl], c)
+
+
 # --------------------------------------------------------------------------------- rows --
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 @pytest.mark.parametrize("fmt", [0, 1])
@@ -200,6 +219,50 @@ def test_gather_rows(dtype, fmt, block, page, hkv, starts, lens):
         # fp32 after the exact stages: at most 5 roundings of 2^-24 of the block's sum |y| / sqrt(b)
         spread = np.abs(y) @ np.abs(s.H)
         assert (np.abs(o[: s.T] - want) <= half * np.abs(want) + 5 * 2.0 ** -24 * spread + 2.0 ** -25).all()
+
+
+def test_gather_rows_many_short_and_empty_sequences():
+    """More sequences than one probe of the offsets holds, most of them empty."""
+    rng = np.random.default_rng(5)
+    lens = np.where(rng.random(300) < 0.8, 0, rng.integers(1, 4, 300))
+    lens[100:170] = 0
+    s = Setup(rng.integers(0, 40, 300), lens, 2, 1, 64, 16, 0).fill()
+    k, v = s.kvq.gather_rows(s.cache, 0, s.dev(s.cu), s.dev(s.before), s.pt, s.T)
+    P = s.host()
+    for kv, out in ((0, k), (1, v)):
+        want = P.values(kv)[s.table[s.seq, s.pos // 16], :, s.pos % 16] @ s.H
+        assert np.abs(out.double().cpu().numpy() - want).max() <= 2.0 ** -10 * np.abs(want).max()
+    # K alone, through the C entry: V is neither read nor written.
+    only, cu, before = s.torch.empty_like(k), s.dev(s.cu), s.dev(s.before)
+    rc = s.kvq.lib().kvq_gather_rows(s.cache.handle, 0, cu.data_ptr(), before.data_ptr(), s.pt.data_ptr(), 300,
+                                     s.T, 0, only.data_ptr(), None,
+                                     s.torch.cuda.current_stream().cuda_stream)
+    assert rc == s.kvq.KVQ_OK and s.torch.equal(only, k) and s.status() == 0
+    # The same sequences as an append and as chunks of queries.
+    a, b = (Setup(rng.integers(0, 40, 300) * 0 + 17, lens, 2, 1, 64, 16, 0) for _ in range(2))
+    x = a.dev(a.rows(a.T, 2).astype(np.float16))
+    zeros = a.torch.zeros(a.T, dtype=a.torch.int32, device="cuda")
+    a.kvq.rope_quant_append(a.cache, 0, x, x, a.dev(a.cu), a.dev(a.before), a.pt,
+                            a.kvq.Rope(a.torch.ones(64, device="cuda")), positions=zeros)
+    b.kvq.rotate_quant_append(b.cache, 0, x, x, b.dev(b.cu), b.dev(b.before), b.pt)
+    assert a.torch.equal(a.pool, b.pool) and a.status() == 0
+
+
+def test_gathered_rows_feed_an_append():
+    """A prefix copied to another layer: read back and appended again, one call after the other (the
+    append reads its k and v early, so the read-back must have completed)."""
+    lens = [9000, 7001]
+    s = Setup([0, 0], lens, 8, 1, 64, 64, 0, layers=2, layer=0).fill()
+    cu, zero = s.dev(s.cu), s.dev(s.before)
+    for _ in range(5):
+        k, v = s.kvq.gather_rows(s.cache, 0, cu, zero, s.pt, s.T)
+        k.zero_(), v.zero_()
+        s.kvq.gather_rows(s.cache, 0, cu, zero, s.pt, s.T, k_out=k, v_out=v)
+        s.kvq.rotate_quant_append(s.cache, 1, k, v, cu, zero, s.pt)
+        got = s.pool.clone()
+        s.torch.cuda.synchronize()
+        s.kvq.rotate_quant_append(s.cache, 1, k, v, cu, zero, s.pt)
+        assert s.torch.equal(got, s.pool)
 
 
 # ------------------------------------------------------------------------------- bounds --
@@ -247,6 +310,13 @@ SELECTS = [
     ([3100], [9], 2, 8, 128, 256, 0, 5, 2, 3, True),
     ([2500, 0, 600], [40, 0, 61], 8, 4, 128, 16, 0, 1, 0, 1, True),
     ([6000], [130], 1, 4, 64, 64, 1, 300, 1, 1, True),
+    ([9000, 700], [1, 1], 1, 1, 64, 16, 0, 20, 1, 1, False),
+    ([4500], [1], 3, 2, 1, 16, 1, 13, 2, 0, False),
+    ([1500, 90], [40, 33], 1, 8, 128, 16, 0, 12, 1, 2, True),
+    ([1500], [50], 1, 2, 32, 16, 1, 20, 2, 1, True),
+    ([1200], [64], 2, 1, 64, 16, 0, 7, 0, 3, True),
+    ([70] * 40, [1] * 40, 2, 4, 64, 16, 0, 3, 1, 1, False),
+    ([70] * 40, [2] * 40, 1, 2, 64, 16, 0, 3, 1, 1, True),
 ]
 
 
@@ -279,6 +349,20 @@ def test_select_blocks(case):
             pg = s.table[b, :n]
             want = ref.choose(q[t, h * group:(h + 1) * group], block, lo[pg, h], hi[pg, h], sg[pg, h], n, nb, sink, recent)
             assert np.array_equal(o[t, h], want), (t, h, o[t, h], want)
+
+
+@pytest.mark.parametrize("extra,new,chunk", [(20000, [19], True), (49000, [1], False)])
+def test_select_blocks_wide_page_table(extra, new, chunk):
+    """A page table far wider than the sequences: the scores of fewer queries fit at a time."""
+    a, b = (Setup([3000], new, 1, 4, 64, 16, 0, extra=x).fill() for x in (extra, 0))
+    q = a.rng.standard_normal((a.T, 4, D)).astype(np.float16)
+    out = []
+    for s in (a, b):
+        bd, *_ = _filled_bounds(s, s.host())
+        out.append(s.kvq.select_blocks(s.cache, 0, s.dev(q), s.dev(s.after), s.pt, bd, 9,
+                                       cu_q=s.dev(s.cu) if chunk else None))
+        assert s.status() == 0
+    assert a.torch.equal(*out)
 
 
 def test_select_blocks_all_scores_equal_takes_the_lowest_pages():
@@ -476,6 +560,60 @@ def test_run_together(fmt, page, block):
         for kv, got in ((0, ko), (1, vo)):
             want = P.values(kv)[S.table[b, p // page], :, p % page] @ S.H
             assert np.abs(got[b].double().cpu().numpy() - want).max() <= 2.0 ** -10 * np.abs(want).max()
+
+
+def test_pool_beyond_32_bit_offsets():
+    """The same calls on a pool of more than 4 GiB, with the sequences in its last pages."""
+    import torch
+    import bit_paged_kv_diag_b200 as kvq
+    hkv, group, page, block = 2, 4, 64, 64
+    lens = [400, 130]
+    rng = np.random.default_rng(2)
+    pages = (1 << 32) // (hkv * page * 132) + 40
+    need = [(n + page) // page + 1 for n in lens]
+    k, v = (torch.from_numpy(rng.standard_normal((sum(lens), hkv, D)).astype(np.float16)).cuda() for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((sum(lens), hkv * group, D)).astype(np.float16)).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu, zero = torch.tensor([0, lens[0], sum(lens)], **i32), torch.zeros(2, **i32)
+    after = torch.tensor(lens, **i32)
+    last = torch.tensor([lens[0] - 1, sum(lens) - 1], device="cuda")
+    rope = kvq.Rope(torch.ones(64, device="cuda") * 0.01)
+    got = []
+    for n in (sum(need), pages):
+        d = kvq.Desc(1, hkv, hkv * group, D, block, page, n, 2, max(need), 0)
+        pool = torch.empty(kvq.pool_bytes(d), dtype=torch.uint8, device="cuda")
+        order = np.arange(n - 1, -1, -1, dtype=np.int32)
+        cache, table = kvq.alloc_pages(d, np.array(lens, np.int32), order, pool=pool)
+        pt, bd = torch.from_numpy(table).cuda(), kvq.BlockBounds.alloc(cache)
+        qr = kvq.rope_quant_append(cache, 0, k, v, cu, zero, pt, rope, q=q)
+        kvq.update_block_bounds(cache, 0, bd, cu, zero, pt, sum(lens))
+        one = qr[last].contiguous()
+        blocks = kvq.select_blocks(cache, 0, one, after, pt, bd, 3)
+        got.append([qr, *kvq.gather_rows(cache, 0, cu, zero, pt, sum(lens)), blocks,
+                    kvq.sparse_attention(cache, 0, one, after, pt, blocks), kvq.decode_attention(cache, 0, one, after, pt)])
+        assert kvq.get_device_status(cache) == 0
+        cache.close()
+        del pool, bd
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_stream_argument():
+    """Calls on a given stream, as an object and as an address, while the current one is another."""
+    import torch
+    s = Setup([100], [1], 2, 4, 64, 16, 0).fill()
+    q = torch.randn(1, 8, D, device="cuda").half()
+    bd, *_ = _filled_bounds(s, s.host())
+    after = s.dev(s.after)
+    want = s.kvq.select_blocks(s.cache, 0, q, after, s.pt, bd, 4)
+    ref_out = s.kvq.sparse_attention(s.cache, 0, q, after, s.pt, want)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for st in (side, side.cuda_stream):
+        blocks = s.kvq.select_blocks(s.cache, 0, q, after, s.pt, bd, 4, stream=st)
+        out = s.kvq.sparse_attention(s.cache, 0, q, after, s.pt, blocks, stream=st)
+        side.synchronize()
+        assert torch.equal(out, ref_out) and torch.equal(blocks, want)
 
 
 # ------------------------------------------------------------------------------- refusals --
