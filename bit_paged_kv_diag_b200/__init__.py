@@ -319,10 +319,11 @@ class Rope:
 
     def __init__(self, inv_freq, interleaved=False, factor=1.0):
         import torch
-        _dev_ptr(inv_freq, "inv_freq", torch.float32)
+        self._ptr = _dev_ptr(inv_freq, "inv_freq", torch.float32)  # checked once: the tensor is kept
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq must have one dimension")
         self.inv_freq = inv_freq
+        self._device = inv_freq.get_device()
         self.rotary_dim = 2 * int(inv_freq.shape[0])
         self.interleaved = bool(interleaved)
         self.factor = float(factor)
@@ -336,10 +337,13 @@ class BlockBounds:
 
     def __init__(self, codes, scale):
         import torch
-        _dev_ptr(codes, "codes", torch.int8)
-        _dev_ptr(scale, "scale", torch.float32)
-        self.codes = codes
+        self._ptrs = _dev_ptr(codes, "codes", torch.int8), _dev_ptr(scale, "scale", torch.float32)
+        if tuple(codes.shape) != (*scale.shape, 2, 128) or scale.dim() != 3:
+            raise ValueError("codes must be [layers][pages][heads][2][128], scale [layers][pages][heads]")
+        self.codes = codes  # (both are checked once and kept)
         self.scale = scale
+        self._shape = tuple(scale.shape)
+        self._device = codes.get_device() if codes.get_device() == scale.get_device() else -1
 
     @classmethod
     def alloc(cls, cache):
@@ -350,9 +354,11 @@ class BlockBounds:
                    torch.zeros(*shape, dtype=torch.float32, device=dev))
 
     def pointers(self, cache):
-        shape = cache.page_shape
-        return (_arg(cache, self.codes, "codes", _torch.int8, (*shape, 2, 128)),
-                _arg(cache, self.scale, "scale", _torch.float32, shape))
+        if self._shape != cache.page_shape:
+            raise ValueError(f"bounds of {self._shape} for a cache of {cache.page_shape}")
+        if self._device != cache.device:
+            raise ValueError(f"bounds must be on cuda:{cache.device}")
+        return self._ptrs
 
 
 def _arg(cache, t, what, dtype, shape):
@@ -443,18 +449,21 @@ def rope_quant_append(cache: Cache, layer: int, k, v, cu_new_tokens, seq_lens, p
     vp, vs = _tokens(cache, v, "v", dtype, (T, cache.kv_heads, 128))
     batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_new_tokens, "cu_new_tokens")
     pos = None if positions is None else _arg(cache, positions, "positions", _torch.int32, (T,))
-    freq = _arg(cache, rope.inv_freq, "inv_freq", _torch.float32, (rope.rotary_dim // 2,))
+    if rope._device != cache.device:
+        raise ValueError(f"inv_freq must be on cuda:{cache.device}")
     qp, qs, op = None, 0, None
     if q is not None:
         shape = (T, cache.q_heads, 128)
         qp, qs = _tokens(cache, q, "q", dtype, shape)
         if q_out is None:
             q_out = _empty(cache, shape, _torch.float16, stream)
-        op = _arg(cache, q_out, "q_out", _torch.float16, shape)
+            op = q_out.data_ptr()
+        else:
+            op = _arg(cache, q_out, "q_out", _torch.float16, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
     _run(cache, stream, "kvq_rope_quant_append", int(layer), code, qp, qs, kp, ks, vp, vs, cu, sl, pos, pt,
-         batch, T, freq, rope.rotary_dim, int(rope.interleaved), rope.factor, op)
+         batch, T, rope._ptr, rope.rotary_dim, int(rope.interleaved), rope.factor, op)
     return q_out
 
 
@@ -467,12 +476,17 @@ def gather_rows(cache: Cache, layer: int, cu_rows, starts, page_table, total_row
     code = _dtype_code(dtype)
     shape = (int(total_rows), cache.kv_heads, 128)
     batch, st, pt, cu = _seqs(cache, starts, page_table, cu_rows, "cu_rows")
-    if k_out is None:
+    if k_out is None and v_out is None and stream is None:
         k_out = _empty(cache, shape, dtype, stream)
-    if v_out is None:
-        v_out = _empty(cache, shape, dtype, stream)
-    _run(cache, stream, "kvq_gather_rows", int(layer), cu, st, pt, batch, shape[0], code,
-         _arg(cache, k_out, "k_out", dtype, shape), _arg(cache, v_out, "v_out", dtype, shape))
+        v_out = _torch.empty_like(k_out)
+        kp, vp = k_out.data_ptr(), v_out.data_ptr()
+    else:
+        if k_out is None:
+            k_out = _empty(cache, shape, dtype, stream)
+        if v_out is None:
+            v_out = _empty(cache, shape, dtype, stream)
+        kp, vp = _arg(cache, k_out, "k_out", dtype, shape), _arg(cache, v_out, "v_out", dtype, shape)
+    _run(cache, stream, "kvq_gather_rows", int(layer), cu, st, pt, batch, shape[0], code, kp, vp)
     return k_out, v_out
 
 
@@ -496,9 +510,12 @@ def select_blocks(cache: Cache, layer: int, q, seq_lens, page_table, bounds: Blo
     batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_q, "cu_q")
     codes, scale = bounds.pointers(cache)
     qp = _arg(cache, q, "q", _torch.float16, (tq, cache.q_heads, 128))
+    shape = (tq, cache.kv_heads, max(nb, 0))
     if blocks is None:
-        blocks = _empty(cache, (tq, cache.kv_heads, max(nb, 0)), _torch.int32, stream)
-    bp = _arg(cache, blocks, "blocks", _torch.int32, (tq, cache.kv_heads, max(nb, 0)))
+        blocks = _empty(cache, shape, _torch.int32, stream)
+        bp = blocks.data_ptr()
+    else:
+        bp = _arg(cache, blocks, "blocks", _torch.int32, shape)
     _run(cache, stream, "kvq_select_blocks", int(layer), codes, scale, qp, cu, sl, pt, batch, tq, nb,
          int(sink), int(recent), bp)
     return blocks
@@ -517,8 +534,10 @@ def sparse_attention(cache: Cache, layer: int, q, seq_lens, page_table, blocks, 
     nb = int(blocks.shape[2])
     bp = _arg(cache, blocks, "blocks", _torch.int32, (tq, cache.kv_heads, nb))
     if out is None:
-        out = _torch.empty_like(q) if stream is None else _empty(cache, (tq, cache.q_heads, 128), _torch.float16, stream)
-    op = _arg(cache, out, "out", _torch.float16, (tq, cache.q_heads, 128))
+        out = _torch.empty_like(q) if stream is None else _empty(cache, q.shape, _torch.float16, stream)
+        op = out.data_ptr()
+    else:
+        op = _arg(cache, out, "out", _torch.float16, (tq, cache.q_heads, 128))
     _run(cache, stream, "kvq_sparse_attention", int(layer), qp, cu, sl, pt, bp, nb, batch, tq,
          float(softmax_scale), op)
     return out

@@ -663,7 +663,10 @@ def test_refusals():
         kvq.gather_rows(c, 0, cu, lens, s.pt, T, k_out=k[:2])
     assert status(lambda: kvq.gather_rows(c, 0, cu, lens, s.pt, T, k_out=odd)) == kvq.KVQ_EINVAL
     with pytest.raises(ValueError):
-        kvq.update_block_bounds(c, 0, kvq.BlockBounds(bd.codes[:, :1].contiguous(), bd.scale), cu, lens, s.pt, T)
+        kvq.BlockBounds(bd.codes[:, :1].contiguous(), bd.scale)
+    with pytest.raises(ValueError):
+        kvq.update_block_bounds(c, 0, kvq.BlockBounds(bd.codes[:, :1].contiguous(), bd.scale[:, :1].contiguous()), cu,
+                                lens, s.pt, T)
     assert status(lambda: kvq.update_block_bounds(c, 0, bd, cu, lens, s.pt, -1)) == kvq.KVQ_EINVAL
 
     def select(nb=4, qq=q, **kw):

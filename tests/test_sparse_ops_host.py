@@ -27,7 +27,7 @@ def test_host_tensors_are_refused():
     with pytest.raises(TypeError):
         kvq.BlockBounds(torch.zeros(1, 4, 2, 2, 128, dtype=torch.int8), torch.zeros(1, 4, 2))
     rope = kvq.Rope.__new__(kvq.Rope)
-    rope.inv_freq, rope.rotary_dim, rope.interleaved, rope.factor = torch.ones(64), 128, False, 1.0
+    rope.rotary_dim, rope.interleaved, rope.factor = 128, False, 1.0
     with pytest.raises(TypeError):
         kvq.rope_quant_append(cache, 0, x, x, cu, i, t, rope, q=q)
     with pytest.raises(TypeError):
