@@ -168,6 +168,14 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return r;
 }
 
+// Two fp32 values -> fp16, nearest even (lo -> low half): one conversion of the pair (two scalar
+// ones go through the special-function unit, which then bounds the q part).
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // 8 values of the inputs' type -> fp16.
 template <bool BF16>
 __device__ __forceinline__ uint4 half_chunk(uint4 v) {
@@ -177,7 +185,7 @@ __device__ __forceinline__ uint4 half_chunk(uint4 v) {
   for (int e = 0; e < 4; e++) {
     float a, b;
     upk(widen<BF16>(w[e]), a, b);
-    o[e] = pack_half2(__float2half_rn(a), __float2half_rn(b));
+    o[e] = half_pair(a, b);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -199,13 +207,13 @@ __device__ __forceinline__ void rotate_chunks(uint4& a, uint4& b, const float (&
       const float y1 = __fmaf_rn(a1, c[2 * e + 1], -__fmul_rn(b1, s[2 * e + 1]));
       const float z0 = __fmaf_rn(b0, c[2 * e], __fmul_rn(a0, s[2 * e]));
       const float z1 = __fmaf_rn(b1, c[2 * e + 1], __fmul_rn(a1, s[2 * e + 1]));
-      oa[e] = pack_half2(__float2half_rn(y0), __float2half_rn(y1));
-      ob[e] = pack_half2(__float2half_rn(z0), __float2half_rn(z1));
+      oa[e] = half_pair(y0, y1);
+      ob[e] = half_pair(z0, z1);
     } else {
       const float y0 = __fmaf_rn(a0, c[e], -__fmul_rn(a1, s[e])), y1 = __fmaf_rn(a1, c[e], __fmul_rn(a0, s[e]));
       const float z0 = __fmaf_rn(b0, c[4 + e], -__fmul_rn(b1, s[4 + e])), z1 = __fmaf_rn(b1, c[4 + e], __fmul_rn(b0, s[4 + e]));
-      oa[e] = pack_half2(__float2half_rn(y0), __float2half_rn(y1));
-      ob[e] = pack_half2(__float2half_rn(z0), __float2half_rn(z1));
+      oa[e] = half_pair(y0, y1);
+      ob[e] = half_pair(z0, z1);
     }
   }
   a = make_uint4(oa[0], oa[1], oa[2], oa[3]);
