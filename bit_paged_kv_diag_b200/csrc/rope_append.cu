@@ -24,7 +24,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
-#include <atomic>
+#include <type_traits>
 
 #include "append_row.cuh"
 #include "kvq_internal.h"
@@ -98,7 +98,10 @@ __device__ __forceinline__ void cos_sin(double theta, double& c, double& s) {
 template <bool BF16>
 __device__ __forceinline__ f2 widen(uint32_t w) {
   if constexpr (BF16) return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  else return pk(cvt_f16(w & 0xFFFFu), cvt_f16(w >> 16));
+  else {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pk(v.x, v.y);
+  }
 }
 
 // Position rotation of one lane's half row.  row: the row in shared memory; raw[t] = its chunk
@@ -193,27 +196,33 @@ __device__ __forceinline__ uint4 half_chunk(uint4 v) {
 // The rotation of two chunks a, b of 8 channels (16-bit values) with the 8 cosines and sines of
 // their pairs: channel e of a with channel e of b, or, interleaved, the pairs inside the chunks.
 template <bool BF16>
-__device__ __forceinline__ void rotate_chunks(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8],
-                                              bool interleaved) {
+__device__ __forceinline__ void rotate_chunks(uint4& a, uint4& b, const f2 (&c)[4], const f2 (&s)[4], bool interleaved) {
   const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
   uint32_t oa[4], ob[4];
+  if (!interleaved) {
 #pragma unroll
-  for (int e = 0; e < 4; e++) {
-    float a0, a1, b0, b1;
-    upk(widen<BF16>(wa[e]), a0, a1);
-    upk(widen<BF16>(wb[e]), b0, b1);
-    if (!interleaved) {
-      const float y0 = __fmaf_rn(a0, c[2 * e], -__fmul_rn(b0, s[2 * e]));
-      const float y1 = __fmaf_rn(a1, c[2 * e + 1], -__fmul_rn(b1, s[2 * e + 1]));
-      const float z0 = __fmaf_rn(b0, c[2 * e], __fmul_rn(a0, s[2 * e]));
-      const float z1 = __fmaf_rn(b1, c[2 * e + 1], __fmul_rn(a1, s[2 * e + 1]));
-      oa[e] = half_pair(y0, y1);
-      ob[e] = half_pair(z0, z1);
-    } else {
-      const float y0 = __fmaf_rn(a0, c[e], -__fmul_rn(a1, s[e])), y1 = __fmaf_rn(a1, c[e], __fmul_rn(a0, s[e]));
-      const float z0 = __fmaf_rn(b0, c[4 + e], -__fmul_rn(b1, s[4 + e])), z1 = __fmaf_rn(b1, c[4 + e], __fmul_rn(b0, s[4 + e]));
-      oa[e] = half_pair(y0, y1);
-      ob[e] = half_pair(z0, z1);
+    for (int e = 0; e < 4; e++) {
+      const f2 x = widen<BF16>(wa[e]), y = widen<BF16>(wb[e]), ns = s[e] ^ 0x8000000080000000ull;
+      float u0, u1, v0, v1;
+      upk(fma2(y, ns, mul2(x, c[e])), u0, u1);
+      upk(fma2(x, s[e], mul2(y, c[e])), v0, v1);
+      oa[e] = half_pair(u0, u1);
+      ob[e] = half_pair(v0, v1);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      float c0, c1, s0, s1;
+      upk(c[e], c0, c1);
+      upk(s[e], s0, s1);
+#pragma unroll
+      for (int i = 0; i < 2; i++) {  // pairs 2e, 2e + 1: chunk a for e < 2, chunk b after
+        const int z = (2 * e + i) & 3;
+        float x, y;
+        upk(widen<BF16>(e < 2 ? wa[z] : wb[z]), x, y);
+        const float cc = i ? c1 : c0, ss = i ? s1 : s0;
+        (e < 2 ? oa : ob)[z] = half_pair(__fmaf_rn(y, -ss, __fmul_rn(x, cc)), __fmaf_rn(x, ss, __fmul_rn(y, cc)));
+      }
     }
   }
   a = make_uint4(oa[0], oa[1], oa[2], oa[3]);
@@ -297,38 +306,40 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
     uint8_t* const o0 = reinterpret_cast<uint8_t*>(p.q_out) +
                         (static_cast<size_t>(t0) * p.num_kv_heads + h0) * p.group * kRow;
     const size_t o_stride = static_cast<size_t>(p.num_kv_heads) * p.group * kRow;
-    for (int st = w; st < nsq; st += kWarps) {
+    // SAME: the four rows belong to one token (its head count is a multiple of four): one address,
+    // one read of the angles.
+    auto q_stage = [&](int st, auto same_token) {
+      constexpr bool SAME = decltype(same_token)::value;
       const int r0 = st * kStageRows + 4 * (lane >> 3);
+      if (r0 >= nq) return;
       int ti = r0 / gq, hq = r0 - ti * gq;
       uint4 a[4], b[4];
       uint8_t* dst[4];
       int tok[4];
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        tok[i] = -1;
-        if (r0 + i < nq) {
-          const uint8_t* src = q0 + static_cast<int64_t>(ti) * p.q_stride * 2 + hq * kRow;
-          a[i] = ldg_stream(src + 16 * ca);
-          b[i] = ldg_stream(src + 16 * cb);
-          dst[i] = o0 + ti * o_stride + hq * kRow;
-          tok[i] = ti;
-          if (++hq == gq) {
-            hq = 0;
-            ti++;
-          }
+        tok[i] = SAME || r0 + i < nq ? ti : -1;
+        if (tok[i] < 0) continue;
+        const uint8_t* src = q0 + static_cast<int64_t>(ti) * p.q_stride * 2 + (SAME ? hq + i : hq) * kRow;
+        a[i] = ldg_stream(src + 16 * ca);
+        b[i] = ldg_stream(src + 16 * cb);
+        dst[i] = o0 + ti * o_stride + (SAME ? hq + i : hq) * kRow;
+        if (!SAME && ++hq == gq) {
+          hq = 0;
+          ti++;
         }
       }
-      float c[8], s[8];
+      f2 c[4], s[4];
       int have = -1;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        if (tok[i] < 0) continue;
-        if (turn && tok[i] != have) {
+        if (!SAME && tok[i] < 0) continue;
+        if (turn && (SAME ? i == 0 : tok[i] != have)) {
           have = tok[i];
-          const float4* src = reinterpret_cast<const float4*>(cs + have * kD + 8 * j);
-          const float4 c0 = src[0], c1 = src[1], s0 = src[kD / 8], s1 = src[kD / 8 + 1];
-          c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-          s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+          const ulonglong2* src = reinterpret_cast<const ulonglong2*>(cs + have * kD + 8 * j);
+          const ulonglong2 c0 = src[0], c1 = src[1], s0 = src[kD / 8], s1 = src[kD / 8 + 1];
+          c[0] = c0.x, c[1] = c0.y, c[2] = c1.x, c[3] = c1.y;
+          s[0] = s0.x, s[1] = s0.y, s[2] = s1.x, s[3] = s1.y;
         }
         if (turn) {
           rotate_chunks<BF16>(a[i], b[i], c, s, p.interleaved);
@@ -340,6 +351,11 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
         stg_128(dst[i] + 16 * ca, a[i].x, a[i].y, a[i].z, a[i].w);
         stg_128(dst[i] + 16 * cb, b[i].x, b[i].y, b[i].z, b[i].w);
       }
+    };
+    if ((gq & 3) == 0) {
+      for (int st = w; st < nsq; st += kWarps) q_stage(st, std::true_type{});
+    } else {
+      for (int st = w; st < nsq; st += kWarps) q_stage(st, std::false_type{});
     }
   }
 
