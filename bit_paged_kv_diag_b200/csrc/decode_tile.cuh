@@ -352,13 +352,16 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 struct Valid {
   int n[2];
 };
-__device__ __forceinline__ Valid prefix_valid(int ntok) { return {{ntok, ntok - 16}}; }
+// Whether token 16 j + tau of a tile is attended: of a tile with a valid prefix of ntok tokens, or
+// with a prefix in each half.
+__device__ __forceinline__ bool tok_valid(int ntok, int j, int tau) { return 16 * j + tau < ntok; }
+__device__ __forceinline__ bool tok_valid(Valid v, int j, int tau) { return tau < v.n[j]; }
 
 // Scores (log2 domain) of an NVFP4 tile, in tile_qk's layout: A row g <-> token tau0,
 // row g + 8 <-> tau1; the lane's 16 code bytes of a token row are channels 32c..32c+31
 // (blocks 2c, 2c + 1), byte 2kk <-> channels 32c + 4kk, +1 (k columns 2c, 2c + 1).
-template <int G, int SEFF>
-__device__ __forceinline__ void tile_qk4(const QFrag4<G>& qf, const uint8_t* slot, Valid ntok, int lane,
+template <int G, int SEFF, typename N>
+__device__ __forceinline__ void tile_qk4(const QFrag4<G>& qf, const uint8_t* slot, N ntok, int lane,
                                          float (&sc)[2][QFrag4<G>::NQ][2]) {
   constexpr int RB = row_bytes(true);
   const int g = lane >> 2, c = lane & 3;
@@ -393,7 +396,7 @@ __device__ __forceinline__ void tile_qk4(const QFrag4<G>& qf, const uint8_t* slo
         if (G == 8) mma_16816(accL, a0, a1, a2, a3, qf.L[G == 8 ? kk : 0][0], qf.L[G == 8 ? kk : 0][1]);
       }
     }
-    const bool v0 = tau0 < ntok.n[j], v1 = tau1 < ntok.n[j];
+    const bool v0 = tok_valid(ntok, j, tau0), v1 = tok_valid(ntok, j, tau1);
     if (G == 8) {
 #pragma unroll
       for (int qq = 0; qq < 2; qq++)
@@ -438,8 +441,8 @@ __device__ __forceinline__ void state_reset(State<G>& st) {
 // PV of the current one sit in one straight-line block the compiler can interleave.
 
 // Scores (log2 domain) of the tile: sc[k-step][owned query][row], -inf past them.
-template <int G, int SEFF>
-__device__ __forceinline__ void tile_qk(const QFrag<G>& qf, const uint8_t* slot, Valid ntok, int lane,
+template <int G, int SEFF, typename N>
+__device__ __forceinline__ void tile_qk(const QFrag<G>& qf, const uint8_t* slot, N ntok, int lane,
                                         float (&sc)[2][QFrag<G>::NQ][2]) {
   const int g = lane >> 2, c = lane & 3;
   const int tau0 = (g < 4) ? g : g + 4;  // token of A row g
@@ -463,7 +466,7 @@ __device__ __forceinline__ void tile_qk(const QFrag<G>& qf, const uint8_t* slot,
     }
     const __half* skp = reinterpret_cast<const __half*>(pbase + SEFF * 128) + sl;
     const float sk0 = __half2float(skp[tau0]), sk1 = __half2float(skp[tau1]);
-    const bool v0 = tau0 < ntok.n[j], v1 = tau1 < ntok.n[j];
+    const bool v0 = tok_valid(ntok, j, tau0), v1 = tok_valid(ntok, j, tau1);
     const float k14 = 1.0f / 16384.0f;
     if (G == 8) {
       // Column 2c = query 2c (qq 0), 2c+1 = query 2c+1 (qq 1); rows g (d0, d1), g+8 (d2, d3).
@@ -542,8 +545,8 @@ __device__ __forceinline__ void split_hi_lo(float p0, float p1, uint32_t& hi, ui
 // PV of the tile with probabilities pr.  B fragment of thread (g, c): tokens c, c+4 (b0)
 // and c+8, c+12 (b1) of the k-step for column g, taken from the lanes that scored them
 // (rows c and c + 4 of the QK^T fragment).
-template <int G, int SEFF>
-__device__ __forceinline__ void tile_pv(State<G>& st, const uint8_t* slot, Valid ntok, int lane,
+template <int G, int SEFF, typename N>
+__device__ __forceinline__ void tile_pv(State<G>& st, const uint8_t* slot, N ntok, int lane,
                                         const float (&pr)[2][QFrag<G>::NQ][2]) {
   const int g = lane >> 2, c = lane & 3;
   const int tau0 = (g < 4) ? g : g + 4;
@@ -557,7 +560,7 @@ __device__ __forceinline__ void tile_pv(State<G>& st, const uint8_t* slot, Valid
     const uint8_t* vb = pbase + SEFF * 64 + sl * 64;
     const __half* svp = reinterpret_cast<const __half*>(pbase + SEFF * 130) + sl;
     const float sv0 = __half2float(svp[tau0]), sv1 = __half2float(svp[tau1]);
-    const bool v0 = tau0 < ntok.n[j], v1 = tau1 < ntok.n[j];
+    const bool v0 = tok_valid(ntok, j, tau0), v1 = tok_valid(ntok, j, tau1);
     // P' = p * s_v carried as fp16 hi + lo (relative precision ~2^-22).
     uint32_t bh0, bh1, bl0 = 0u, bl1 = 0u;
     if (G == 8) {
@@ -626,8 +629,8 @@ __device__ __forceinline__ uint32_t bitsel(uint32_t a, uint32_t b, uint32_t m) {
 // PV of an NVFP4 tile with probabilities pr: as tile_pv, with P' = p; the V scales are
 // applied in the dequantised A operand (the lane's channels 16g..16g+15 are block g of
 // each token row, so a register's two tokens each take their own scale).
-template <int G, int SEFF>
-__device__ __forceinline__ void tile_pv4(State<G>& st, const uint8_t* slot, Valid ntok, int lane,
+template <int G, int SEFF, typename N>
+__device__ __forceinline__ void tile_pv4(State<G>& st, const uint8_t* slot, N ntok, int lane,
                                          const float (&pr)[2][QFrag4<G>::NQ][2]) {
   constexpr int RB = row_bytes(true);
   const int g = lane >> 2, c = lane & 3;
@@ -641,7 +644,7 @@ __device__ __forceinline__ void tile_pv4(State<G>& st, const uint8_t* slot, Vali
     const int sl = (16 * j) % SEFF;
     const uint8_t* vb = pbase + SEFF * 64 + sl * 64;
     const uint8_t* vs = pbase + SEFF * 128 + SEFF * 8 + sl * 8;  // V scales [token][8]
-    const bool v0 = tau0 < ntok.n[j], v1 = tau1 < ntok.n[j];
+    const bool v0 = tok_valid(ntok, j, tau0), v1 = tok_valid(ntok, j, tau1);
     uint32_t bh0, bh1, bl0 = 0u, bl1 = 0u;
     if (G == 8) {
       uint32_t xh[2], xl[2];
@@ -675,9 +678,8 @@ __device__ __forceinline__ void tile_pv4(State<G>& st, const uint8_t* slot, Vali
     const uint2 t3 = *reinterpret_cast<const uint2*>(vb + (c + 12) * 64 + 8 * g);
     // Tokens past the sequence's end take scale 0: their slot bytes are whatever the pool or
     // an earlier tile left there, and an E4M3 NaN would survive the zero probability.
-    const int left = ntok.n[j] - c;
-    const uint32_t s0 = left > 0 ? vs[(c + 0) * 8 + g] : 0u, s1 = left > 4 ? vs[(c + 4) * 8 + g] : 0u;
-    const uint32_t s2 = left > 8 ? vs[(c + 8) * 8 + g] : 0u, s3 = left > 12 ? vs[(c + 12) * 8 + g] : 0u;
+    const uint32_t s0 = tok_valid(ntok, j, c) ? vs[(c + 0) * 8 + g] : 0u, s1 = tok_valid(ntok, j, c + 4) ? vs[(c + 4) * 8 + g] : 0u;
+    const uint32_t s2 = tok_valid(ntok, j, c + 8) ? vs[(c + 8) * 8 + g] : 0u, s3 = tok_valid(ntok, j, c + 12) ? vs[(c + 12) * 8 + g] : 0u;
     const uint32_t s01 = s0 | (s1 << 8), s23 = s2 | (s3 << 8);
     const uint32_t S01 = e4m3x2_to_f16x2(s01), S23 = e4m3x2_to_f16x2(s23);
     const uint32_t w0[2] = {t0.x, t0.y}, w1[2] = {t1.x, t1.y};
@@ -894,19 +896,19 @@ __device__ __forceinline__ void qfrag_get(QFrag4<G>& f, const uint32_t* qfb, con
   qfrag4_load<G>(f, qfb, sfb, lane);
 }
 
-template <int G, int SEFF>
-__device__ __forceinline__ void tile_qk_any(const QFrag<G>& qf, const uint8_t* slot, Valid ntok, int lane,
+template <int G, int SEFF, typename N>
+__device__ __forceinline__ void tile_qk_any(const QFrag<G>& qf, const uint8_t* slot, N ntok, int lane,
                                             float (&sc)[2][QFrag<G>::NQ][2]) {
   tile_qk<G, SEFF>(qf, slot, ntok, lane, sc);
 }
-template <int G, int SEFF>
-__device__ __forceinline__ void tile_qk_any(const QFrag4<G>& qf, const uint8_t* slot, Valid ntok, int lane,
+template <int G, int SEFF, typename N>
+__device__ __forceinline__ void tile_qk_any(const QFrag4<G>& qf, const uint8_t* slot, N ntok, int lane,
                                             float (&sc)[2][QFrag4<G>::NQ][2]) {
   tile_qk4<G, SEFF>(qf, slot, ntok, lane, sc);
 }
 
-template <int G, int SEFF, bool FP4>
-__device__ __forceinline__ void tile_pv_any(State<G>& st, const uint8_t* slot, Valid ntok, int lane,
+template <int G, int SEFF, bool FP4, typename N>
+__device__ __forceinline__ void tile_pv_any(State<G>& st, const uint8_t* slot, N ntok, int lane,
                                             const float (&pr)[2][QFrag<G>::NQ][2]) {
   if constexpr (FP4) tile_pv4<G, SEFF>(st, slot, ntok, lane, pr);
   else tile_pv<G, SEFF>(st, slot, ntok, lane, pr);
