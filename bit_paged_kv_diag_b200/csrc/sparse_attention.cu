@@ -214,8 +214,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
   uint32_t parity = 0;
   bool dead = false;
   auto valid_of = [&](int s) {
+    // (the form that suits the format, as in the decode kernel; two pages need a prefix each)
     const int2 v = valid_ring[w][s];
-    return Valid{{v.x, v.y}};
+    if constexpr (FP4 && kPPT == 1) return v.x;
+    else return Valid{{v.x, v.y}};
   };
   if (issued > 0) {
     if (!mbar_wait_bounded(bar_s, 0u, kWaitLimitNs)) {
