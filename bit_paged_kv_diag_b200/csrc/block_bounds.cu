@@ -14,6 +14,10 @@
 // Half a warp takes a row, lane j of a half the channels 8j .. 8j + 7.  A half's rows go in pairs,
 // so that each nibble expansion yields one channel of two rows and the running bounds take
 // three-operand minima and maxima; the halves meet once at the end.
+//
+// Measured: 8 x 8192 INT4 tokens in pages of 64, 8 heads: 19.8 us for 38 MB (5.8 us at the copy
+// rate); the arithmetic pipe (conversions, minima, maxima) is busy for 61 % of it.  The last pages
+// of 256 sequences: 7.0 us, a chain of four memory round trips.
 #include <cuda_fp16.h>
 #include <math_constants.h>
 #include <stdint.h>

@@ -17,9 +17,16 @@
 // for all heads into a table there, and its warps take stages of 16 rows.
 //   q: 8 lanes a row, lane j the two 8-channel chunks of the pairs 8 j .. 8 j + 7, so a pair
 //      never leaves a lane and the cosines stay in registers from row to row; global memory to
-//      registers and back, no shared memory (a row costs 15 warp instructions; two lanes a row,
+//      registers and back, no shared memory (a row costs 22 warp instructions; two lanes a row,
 //      each computing both partners' products, cost 77).
-//   k, v: two lanes a row, as in the append kernel.
+//   k, v: two lanes a row, as in the append kernel.  (Eight lanes a row straight from global memory
+//      repeat the scale's divisions and the addresses four times as often: 349 us against 303.)
+// Measured, 8 x 8192 tokens, 32 + 2 x 8 heads, INT4, b = 128: 274 us, 5.1 TB/s of algorithmic
+// bytes; 0.79 of the time that they take at the copy rate.  139 M warp instructions at 46 % of the
+// issue slots with 16 warps per SM (126 registers): memory latency at a tile's start and the
+// butterfly's dependency chains share the rest.  Not kept: one persistent CTA per slot with the
+// next tile's copies in flight (registers spill: 503 us); copies issued only after the tokens'
+// places are known (352 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
