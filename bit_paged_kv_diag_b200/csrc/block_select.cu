@@ -24,7 +24,8 @@
 // Choice.  Keys are the scores as ordered 32-bit integers.  The k-th largest is found by counting
 // the keys in 256 equal bins between the smallest and the largest, then inside the bin where the
 // k-th falls, and so on: the range shrinks by 2^8 a round, and the search ends as soon as a bin is
-// taken whole, mostly after two rounds (a bisection takes about 20 passes over the keys).  The
+// taken whole, or its keys fit a warp and are ranked against one another (a bisection takes about
+// 20 passes over the keys).  The
 // pages are then written in ascending order from ballot masks.  A team of warps shares a query.
 //
 // Measured: 464 queries, 8 KV heads, G = 4, up to 1024 pages: 41 us in one wave of 264 CTAs, about
@@ -86,6 +87,13 @@ __device__ __forceinline__ u32x8 ldg_256(const void* p) {
                  "=r"(r.w[7])
                : "l"(p));
   return r;
+}
+
+// Add 1 to a word of shared memory if `on` (predicated: no branch).
+__device__ __forceinline__ void count_if(uint32_t addr, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(addr),
+               "r"(static_cast<uint32_t>(on))
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -307,14 +315,24 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
         sg[r][0] = __shfl_sync(kFull, sigma[r], 8 * c);
         sg[r][1] = __shfl_sync(kFull, sigma[r], 8 * c + 4);
       }
-      auto put = [&](int q, int lp, float v, float factor) {
+      // Keys of n pages of query q, then their stores (the keys' chains interleave).
+      auto put = [&](int q, const auto& lp, const auto& v, const auto& factor) {
+        constexpr int kPut = sizeof(lp) / sizeof(int);
+        const unsigned span = static_cast<unsigned>(max(pages_of(q) - p.recent - p.sink, 0));
+        uint32_t key[kPut];
+#pragma unroll
+        for (int i = 0; i < kPut; i++) {
+          key[i] = ordered(v[i], factor[i]);
+          // (always taken, or behind the query: one unsigned comparison for both ends)
+          if (static_cast<unsigned>(lp[i] - p.sink) >= span) key[i] = 0u;
+        }
         if (q >= nq) return;
-        uint32_t key = ordered(v, factor);
-        // (always taken, or behind the query: one unsigned comparison for both ends)
-        if (static_cast<unsigned>(lp - p.sink) >= static_cast<unsigned>(max(pages_of(q) - p.recent - p.sink, 0))) key = 0u;
-        const uint32_t dst = keys0 + static_cast<uint32_t>(q * KW + lp) * 4;
-        if (CLUSTER) st_cluster(dst, key);
-        else sts_32(dst, key);
+        const uint32_t dst = keys0 + static_cast<uint32_t>(q * KW) * 4;
+#pragma unroll
+        for (int i = 0; i < kPut; i++) {
+          if (CLUSTER) st_cluster(dst + lp[i] * 4, key[i]);
+          else sts_32(dst + lp[i] * 4, key[i]);
+        }
       };
 #pragma unroll 1
       for (int j = 0; j < nrow / 16; j++) {
@@ -337,40 +355,59 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
         const uint64_t S0 = f2_pack(s0, s0), S1 = f2_pack(s1, s1), MM = f2_pack(kMagic, kMagic);
         const int lp0 = mt * kTilePages + 2 * c;
         const int odd = g & 1, high = (g >> 1) & 1;
-        float t[kN];
+        float v[kN][4];
 #pragma unroll
-        for (int r = 0; r < kN; r++) {
-          float v[4];
+        for (int r = 0; r < kN; r++)
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
             const uint64_t d = f2_sub(f2_pack(__int_as_float(acc[r][e]), __int_as_float(acc[r][e + 1])), MM);
             const float2 w2 = f2_unpack(f2_mul(d, e ? S1 : S0));
-            v[e] = w2.x;
-            v[e + 1] = w2.y;
+            v[r][e] = w2.x;
+            v[r][e + 1] = w2.y;
           }
-          const int lp = lp0 + 8 * r;
-          if constexpr (G == 1) {
+        if constexpr (G <= 2) {
+          // Every lane stores all its pages: of rows g and g + 8 (G = 1), or of their maximum.
 #pragma unroll
-            for (int e = 0; e < 4; e++) put(16 * j + g + (e < 2 ? 0 : 8), lp + (e & 1), v[e], sg[r][e & 1]);
-          } else {
-            const float u0 = fmaxf(v[0], v[2]), u1 = fmaxf(v[1], v[3]);
-            if constexpr (G == 2) {
-              put(8 * j + g, lp, u0, sg[r][0]);
-              put(8 * j + g, lp + 1, u1, sg[r][1]);
-            } else {
-              // Lanes g and g ^ 1 share a query: the odd one keeps the odd page.
-              const float other = __shfl_xor_sync(kFull, odd ? u0 : u1, 4);
-              t[r] = fmaxf(odd ? u1 : u0, other);
-              if constexpr (G == 4) {
-                put(4 * j + (g >> 1), lp + odd, t[r], odd ? sg[r][1] : sg[r][0]);
-              } else if (r & 1) {
-                // ... and g ^ 2: the one with that bit set keeps the second of two MMA tiles.
-                const float far = __shfl_xor_sync(kFull, high ? t[r - 1] : t[r], 8);
-                const float best = fmaxf(high ? t[r] : t[r - 1], far);
-                const float f = high ? (odd ? sg[r][1] : sg[r][0]) : (odd ? sg[r - 1][1] : sg[r - 1][0]);
-                put(2 * j + (g >> 2), lp - (high ? 0 : 8) + odd, best, f);
+          for (int x = 0; x < 2; x++) {
+            if (G == 2 && x) break;
+            int lp[2 * kN];
+            float u[2 * kN], f[2 * kN];
+#pragma unroll
+            for (int r = 0; r < kN; r++)
+#pragma unroll
+              for (int e = 0; e < 2; e++) {
+                lp[2 * r + e] = lp0 + 8 * r + e;
+                u[2 * r + e] = G == 2 ? fmaxf(v[r][e], v[r][2 + e]) : v[r][2 * x + e];
+                f[2 * r + e] = sg[r][e];
               }
+            put(G == 2 ? 8 * j + g : 16 * j + 8 * x + g, lp, u, f);
+          }
+        } else {
+          // Lanes g and g ^ 1 share a query: the odd one keeps the odd pages.
+          float t[kN], f[kN];
+#pragma unroll
+          for (int r = 0; r < kN; r++) {
+            const float u0 = fmaxf(v[r][0], v[r][2]), u1 = fmaxf(v[r][1], v[r][3]);
+            t[r] = fmaxf(odd ? u1 : u0, __shfl_xor_sync(kFull, odd ? u0 : u1, 4));
+            f[r] = odd ? sg[r][1] : sg[r][0];
+          }
+          if constexpr (G == 4) {
+            int lp[kN];
+#pragma unroll
+            for (int r = 0; r < kN; r++) lp[r] = lp0 + 8 * r + odd;
+            put(4 * j + (g >> 1), lp, t, f);
+          } else {
+            // ... and g ^ 2: the one with that bit set keeps the second of two MMA tiles.
+            int lp[kN / 2];
+            float u[kN / 2], fh[kN / 2];
+#pragma unroll
+            for (int r = 0; r < kN / 2; r++) {
+              const float far = __shfl_xor_sync(kFull, high ? t[2 * r] : t[2 * r + 1], 8);
+              u[r] = fmaxf(high ? t[2 * r + 1] : t[2 * r], far);
+              fh[r] = high ? f[2 * r + 1] : f[2 * r];
+              lp[r] = lp0 + 16 * r + (high ? 8 : 0) + odd;
             }
+            put(2 * j + (g >> 2), lp, u, fh);
           }
         }
       }
@@ -406,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
     parity ^= 1;
   };
   int* const bins = hist[team * TW];
+  const uint32_t bins_s = smem_addr(bins);
   for (int q = team; q < nq; q += kWarps / TW) {
     const int np = pages_of(q);
     int32_t* out = p.blocks + (static_cast<size_t>(t0 + q) * p.num_kv_heads + h) * k;
@@ -455,8 +493,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
         each4([&](uint4 v) {
           const uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int z = 0; z < 4; z++)
-            if (e[z] - lo <= width) atomicAdd(bins + ((e[z] - lo) >> sh), 1);
+          for (int z = 0; z < 4; z++) count_if(bins_s + ((e[z] - lo) >> sh) * 4, e[z] - lo <= width);
         });
         team_sync();
         // Bins from the top: lane j holds bins 255 - 8 j .. 248 - 8 j.
@@ -499,6 +536,38 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
           break;
         }
         hi = lo + min(hi - lo, (1u << sh) - 1u);
+        if (inbin <= 32) {
+          // Few keys are left: collect them, a lane each, and rank them against one another.
+          if (tw == 0) bins[lane] = 0;
+          if (tw == 0 && lane == 0) bins[32] = 0;
+          team_sync();
+          const uint32_t span = hi - lo;
+          each4([&](uint4 v) {
+            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int z = 0; z < 4; z++)
+              if (e[z] - lo <= span) bins[atomicAdd(bins + 32, 1)] = static_cast<int>(e[z]);
+          });
+          team_sync();
+          const uint32_t mine = static_cast<uint32_t>(bins[lane]);  // 0: none
+          int higher = 0, same = 0;
+          for (int i = 0; i < inbin; i++) {
+            const uint32_t other = __shfl_sync(kFull, mine, i);
+            higher += other > mine;
+            same += other == mine;
+          }
+          const bool it = lane < inbin && higher < need && higher + same >= need;
+          const int src2 = __ffs(__ballot_sync(kFull, it)) - 1;
+          T = __shfl_sync(kFull, mine, src2);
+          higher = __shfl_sync(kFull, higher, src2);
+          same = __shfl_sync(kFull, same, src2);
+          team_sync();  // the list is read
+          if (higher + same != need) {
+            quota = need - higher;
+            T += 1u;
+          }
+          break;
+        }
       }
     }
     // The pages in ascending order: each warp of the team a contiguous part; lane i of a warp
@@ -520,12 +589,14 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
         const uint32_t key = kq[(base + i) * 32 + lane];
         const uint32_t ms = __ballot_sync(kFull, key >= T && need_any);
         if (lane == i) sure = ms;
-        if (quota) {
-          const uint32_t mt = __ballot_sync(kFull, key == T - 1u);
+      }
+      sure |= forced;
+      if (quota) {
+        for (int i = 0; i < m; i++) {
+          const uint32_t mt = __ballot_sync(kFull, kq[(base + i) * 32 + lane] == T - 1u);
           if (lane == i) tie = mt;
         }
       }
-      sure |= forced;
     };
     int before = 0, ties = 0;  // sure and tied pages of the team's earlier warps
     uint32_t sure = 0, tie = 0;
