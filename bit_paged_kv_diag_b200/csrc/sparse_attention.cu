@@ -52,25 +52,28 @@ struct Tiles {
   static constexpr int kBatch = 32 / kPPT;                                  // tiles of a batch
 };
 
-// Where a unit's lists and limits are.
+// Where a unit's pages and limits are.
 struct UnitInfo {
-  const int32_t* list;   // the unit's blocks
   const int32_t* table;  // the sequence's page-table row
   int pos;               // the query's position (-1: nothing to attend)
   int h;
 };
 
-// Entry of this lane: tile x of the unit, page lane % kPPT of the tile (none when x >= x1).
-template <int SEFF, bool FP4>
-__device__ __forceinline__ Entry load_entry(int x, int x1, int lane, const UnitInfo& u, const DecodeParams& p,
-                                            const SparseParams& sp) {
+// This lane's page of tile x of the unit: its place in the list (page lane % kPPT of the tile) and
+// its first token in the page; negative: none.
+template <int SEFF>
+__device__ __forceinline__ int load_block(int x, int x1, int lane, const int32_t* list, const DecodeParams& p,
+                                          const SparseParams& sp) {
   constexpr int kPPT = Tiles<SEFF>::kPPT;
-  Entry e = {0, 0};
-  if (x >= x1) return e;
   const int j = SEFF < kTileTokens ? x * kPPT + lane % kPPT : (x * kTileTokens) >> p.page_shift;
-  if (j >= sp.num_blocks) return e;
+  return x < x1 && j < sp.num_blocks ? __ldcg(list + j) : -1;
+}
+
+// Entry of this lane: logical page blk for tile x.
+template <int SEFF, bool FP4>
+__device__ __forceinline__ Entry make_entry(int x, int blk, const UnitInfo& u, const DecodeParams& p) {
+  Entry e = {0, 0};
   const int off = SEFF < kTileTokens ? 0 : (x * kTileTokens) & (p.page_size - 1);
-  const int blk = __ldcg(u.list + j);
   if (blk < 0 || blk > (u.pos >> p.page_shift)) return e;  // (an arithmetic shift: -1 stays below 0)
   const int left = u.pos + 1 - (blk << p.page_shift) - off;
   if (left <= 0) return e;
@@ -142,6 +145,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
   __syncwarp();
   griddep_wait();
 
+  // q and the first batch of the list are on their way before anything else is looked up: behind
+  // the first tiles' copies they would wait for those.
+  uint4 qv = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < G * kD / 8)
+    qv = __ldcg(reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(t) * p.num_kv_heads + h) * G * kD) + tid);
+  // This warp's tiles: x0 + w, x0 + w + kWarps, ... < x1.
+  const int ntile = (sp.num_blocks * p.page_size + kTileTokens - 1) / kTileTokens;
+  const int x0 = static_cast<int>(static_cast<long long>(ntile) * part / splits);
+  const int x1 = static_cast<int>(static_cast<long long>(ntile) * (part + 1) / splits);
+  const int nT = max(0, (x1 - x0 - w + kWarps - 1) / kWarps);
+  const int32_t* const list = sp.blocks + static_cast<size_t>(unit) * sp.num_blocks;
+  const int xl = x0 + w + kWarps * (lane / kPPT);  // this lane's tile of the first batch
+  const int blk0 = load_block<SEFF>(xl, x1, lane, list, p, sp);
+
   // The query's sequence and position.
   int b = t, pos;
   if (sp.cu_q) {
@@ -158,16 +175,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
     pos = -1;
   }
   UnitInfo u;
-  u.list = sp.blocks + static_cast<size_t>(unit) * sp.num_blocks;
   u.table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
   u.pos = pos;
   u.h = h;
 
-  // This warp's tiles: x0 + w, x0 + w + kWarps, ... < x1.
-  const int ntile = (sp.num_blocks * p.page_size + kTileTokens - 1) / kTileTokens;
-  const int x0 = static_cast<int>(static_cast<long long>(ntile) * part / splits);
-  const int x1 = static_cast<int>(static_cast<long long>(ntile) * (part + 1) / splits);
-  const int nT = max(0, (x1 - x0 - w + kWarps - 1) / kWarps);
   uint8_t* const ring_w = ring + w * kRing<FP4> * kSlot;
   const uint32_t ring_s = smem_addr(ring_w);
   // Producer: batches of kBatch tiles; `todo` holds the batch's tiles that have a token.
@@ -175,9 +186,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
   unsigned todo = 0;
   Entry cur = {0, 0};
   auto fetch = [&](int first) {
-    return load_entry<SEFF, FP4>(x0 + w + kWarps * (first + lane / kPPT), x1, lane, u, p, sp);
+    const int x = xl + kWarps * first;
+    return make_entry<SEFF, FP4>(x, load_block<SEFF>(x, x1, lane, list, p, sp), u, p);
   };
-  Entry nxt = fetch(0);
+  Entry nxt = make_entry<SEFF, FP4>(xl, blk0, u, p);
   int issued = 0;
   auto produce = [&]() {  // issue the next tile that has a token, if any
     while (todo == 0) {
@@ -202,10 +214,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
   for (int i = 0; i < kRing<FP4>; i++) produce();
 
   // q of the unit: rotated and cut by all warps.
-  {
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(t) * p.num_kv_heads + h) * G * kD);
-    for (int i = tid; i < G * kD / 8; i += kThreads) reinterpret_cast<uint4*>(qraw)[i] = __ldcg(src + i);
-  }
+  if (tid < G * kD / 8) reinterpret_cast<uint4*>(qraw)[tid] = qv;
   __syncthreads();
   prep_q<G, kWarps, FP4>(qraw, frag, sf, lane, p, w);
   __syncthreads();
