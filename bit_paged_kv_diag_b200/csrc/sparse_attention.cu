@@ -89,33 +89,41 @@ __device__ __forceinline__ Entry make_entry(int x, int blk, const UnitInfo& u, c
   return e;
 }
 
-// Bulk copies of one tile into a ring slot (the whole warp; lane j < kPPT holds page j's entry).
+// What one lane copies of a tile.  Pages of up to 32 tokens: lane j < kPPT the whole block of page j;
+// larger pages: lanes 0-3 the tile's K codes, V codes, K scales and V scales.
+struct Piece {
+  uint32_t src, per_token;  // byte of the page block, and bytes for each token before the tile's first
+  uint32_t dst, bytes;      // place in the slot; 0 bytes: nothing to copy
+};
 template <int SEFF, bool FP4>
-__device__ __forceinline__ void issue_tile(Entry e, uint32_t slot, uint32_t bar, int lane, const DecodeParams& p) {
+__device__ __forceinline__ Piece piece_of(int lane, int S) {
   constexpr int kPPT = Tiles<SEFF>::kPPT;
-  const int S = p.page_size;
+  constexpr uint32_t SC = FP4 ? kD / 16 : 2;  // scale bytes of a row
+  const uint32_t s = static_cast<uint32_t>(S);
   if (SEFF < kTileTokens || S == kTileTokens) {
-    const bool have = lane < kPPT && e.ntok > 0;
-    const uint32_t blk_bytes = static_cast<uint32_t>(S) * row_bytes(FP4);
-    const int npg = __popc(__ballot_sync(kFull, have));
-    if (lane == 0) mbar_arrive_expect_tx(bar, npg * blk_bytes);
-    __syncwarp();
-    if (have)
-      bulk_copy_g2s(slot + lane * blk_bytes, reinterpret_cast<const void*>(e.addr), blk_bytes, bar, 0ull);
-  } else {
-    // Lanes 0-3 copy the tile's K codes, V codes, K scales and V scales.
-    const uint64_t e0 = __shfl_sync(kFull, e.addr, 0);
-    const uint8_t* blk = reinterpret_cast<const uint8_t*>(e0 & ~static_cast<uint64_t>(15));
-    const size_t o = static_cast<size_t>(e0 & 7u) * kTileTokens;
-    constexpr int SC = FP4 ? kD / 16 : 2;  // scale bytes of a row
-    const uint8_t* src = blk + o * 64;
-    uint32_t dst = slot, bytes = 64 * kTileTokens;
-    if (lane == 1) { src = blk + static_cast<size_t>(S) * 64 + o * 64; dst = slot + 64 * kTileTokens; }
-    if (lane == 2) { src = blk + static_cast<size_t>(S) * 128 + o * SC; dst = slot + 128 * kTileTokens; bytes = SC * kTileTokens; }
-    if (lane == 3) { src = blk + static_cast<size_t>(S) * (128 + SC) + o * SC; dst = slot + (128 + SC) * kTileTokens; bytes = SC * kTileTokens; }
-    if (lane == 0) mbar_arrive_expect_tx(bar, slot_bytes(FP4));
-    __syncwarp();
-    if (lane < 4) bulk_copy_g2s(dst, src, bytes, bar, 0ull);
+    const uint32_t blk = s * row_bytes(FP4);
+    return {0u, 0u, lane * blk, lane < kPPT ? blk : 0u};
+  }
+  if (lane == 0) return {0u, 64u, 0u, 64u * kTileTokens};
+  if (lane == 1) return {s * 64, 64u, 64u * kTileTokens, 64u * kTileTokens};
+  if (lane == 2) return {s * 128, SC, 128u * kTileTokens, SC * kTileTokens};
+  if (lane == 3) return {s * (128 + SC), SC, (128 + SC) * kTileTokens, SC * kTileTokens};
+  return {0u, 0u, 0u, 0u};
+}
+
+// Bulk copies of one tile into a ring slot (the whole warp; with one page per tile every lane holds
+// its entry, with two lane j < 2 page j's).
+template <int SEFF, bool FP4>
+__device__ __forceinline__ void issue_tile(Entry e, const Piece& c, uint32_t slot, uint32_t bar, int lane) {
+  constexpr int kPPT = Tiles<SEFF>::kPPT;
+  uint32_t total = slot_bytes(FP4);
+  if (kPPT == 2) total = __popc(__ballot_sync(kFull, lane < kPPT && e.ntok > 0)) * c.bytes;  // (lane 0's: one block)
+  if (lane == 0) mbar_arrive_expect_tx(bar, total);
+  __syncwarp();
+  if (c.bytes && e.ntok > 0) {
+    const uint8_t* blk = reinterpret_cast<const uint8_t*>(e.addr & ~static_cast<uint64_t>(15));
+    const uint32_t off = c.src + static_cast<uint32_t>(e.addr & 7u) * kTileTokens * c.per_token;
+    bulk_copy_g2s(slot + c.dst, blk + off, c.bytes, bar, 0ull);
   }
 }
 
@@ -190,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
     return make_entry<SEFF, FP4>(x, load_block<SEFF>(x, x1, lane, list, p, sp), u, p);
   };
   Entry nxt = make_entry<SEFF, FP4>(xl, blk0, u, p);
-  int issued = 0;
+  int issued = 0, next_slot = 0;
+  const Piece piece = piece_of<SEFF, FP4>(lane, p.page_size);
   auto produce = [&]() {  // issue the next tile that has a token, if any
     while (todo == 0) {
       tb += kBatch;
@@ -202,13 +211,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
     }
     const int i = __ffs(todo) - 1;  // lane of the tile's first page
     todo &= todo - 1;
+    const int from = kPPT == 2 ? (i + (lane & 1)) & 31 : i;
     Entry e;
-    e.addr = __shfl_sync(kFull, cur.addr, (i + lane) & 31);
-    e.ntok = __shfl_sync(kFull, cur.ntok, (i + lane) & 31);
-    const int n0 = __shfl_sync(kFull, e.ntok, 0), n1 = __shfl_sync(kFull, e.ntok, 1);
-    const int s = issued % kRing<FP4>;
-    if (lane == 0) valid_ring[w][s] = kPPT == 2 ? make_int2(n0, n1) : make_int2(n0, n0 - 16);
-    issue_tile<SEFF, FP4>(e, ring_s + s * kSlot, bar_s + 8 * s, lane, p);
+    e.addr = __shfl_sync(kFull, cur.addr, from);
+    e.ntok = __shfl_sync(kFull, cur.ntok, from);
+    const int s = next_slot;
+    next_slot = s + 1 == kRing<FP4> ? 0 : s + 1;
+    if (kPPT == 2) {
+      if (lane < 2) reinterpret_cast<int*>(&valid_ring[w][s])[lane] = e.ntok;
+    } else if (lane == 0) {
+      valid_ring[w][s] = make_int2(e.ntok, e.ntok - 16);
+    }
+    issue_tile<SEFF, FP4>(e, piece, ring_s + s * kSlot, bar_s + 8 * s, lane);
     issued++;
   };
   for (int i = 0; i < kRing<FP4>; i++) produce();
