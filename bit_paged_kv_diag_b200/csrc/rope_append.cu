@@ -31,8 +31,6 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "append_row.cuh"
 #include "kvq_internal.h"
 #include "kvq_ptx.cuh"
@@ -115,7 +113,7 @@ __device__ __forceinline__ f2 widen(uint32_t w) {
 // t ^ rho (of the lane's half l); cs: the token's cosines [64], then sines [64]; x[4t + e] =
 // channels 2e, 2e + 1 of chunk t ^ rho after the rotation.  Chunks are 8 channels and
 // rotary_dim is a multiple of 16, so a chunk's partner is a whole chunk.
-template <bool BF16>
+template <bool BF16, bool INTER>
 __device__ __forceinline__ void rope_row(const uint4 (&raw)[8], uint32_t row, uint32_t cs, int rho, int l,
                                          const RopeAppendParams& p, f2 (&x)[32]) {
   const int half = p.rotary_dim >> 4;  // chunks in half of the rotated channels
@@ -126,7 +124,7 @@ __device__ __forceinline__ void rope_row(const uint4 (&raw)[8], uint32_t row, ui
 #pragma unroll
     for (int e = 0; e < 4; e++) x[4 * t + e] = widen<BF16>(w[e]);
     if (c >= 2 * half) continue;
-    if (!p.interleaved) {
+    if constexpr (!INTER) {
       const bool lower = c < half;
       const int fc = lower ? c : c - half;
       const uint4 other = lds_128(row + 16 * (lower ? c + half : c - half));
@@ -202,11 +200,11 @@ __device__ __forceinline__ uint4 half_chunk(uint4 v) {
 
 // The rotation of two chunks a, b of 8 channels (16-bit values) with the 8 cosines and sines of
 // their pairs: channel e of a with channel e of b, or, interleaved, the pairs inside the chunks.
-template <bool BF16>
-__device__ __forceinline__ void rotate_chunks(uint4& a, uint4& b, const f2 (&c)[4], const f2 (&s)[4], bool interleaved) {
+template <bool BF16, bool INTER>
+__device__ __forceinline__ void rotate_chunks(uint4& a, uint4& b, const f2 (&c)[4], const f2 (&s)[4]) {
   const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
   uint32_t oa[4], ob[4];
-  if (!interleaved) {
+  if constexpr (!INTER) {
 #pragma unroll
     for (int e = 0; e < 4; e++) {
       const f2 x = widen<BF16>(wa[e]), y = widen<BF16>(wb[e]), ns = s[e] ^ 0x8000000080000000ull;
@@ -236,7 +234,7 @@ __device__ __forceinline__ void rotate_chunks(uint4& a, uint4& b, const f2 (&c)[
   b = make_uint4(ob[0], ob[1], ob[2], ob[3]);
 }
 
-template <int BLOCK, bool FP4, bool BF16>
+template <int BLOCK, bool FP4, bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendParams p) {
   griddep_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];
@@ -307,62 +305,58 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
   {
     const int j = lane & 7, tasks = p.rotary_dim >> 4;
     const bool turn = j < tasks;
-    const int ca = turn && !p.interleaved ? j : 2 * j, cb = turn && !p.interleaved ? j + tasks : 2 * j + 1;
+    const int ca = turn && !INTER ? j : 2 * j, cb = turn && !INTER ? j + tasks : 2 * j + 1;
     const uint8_t* const q0 = static_cast<const uint8_t*>(p.q) + static_cast<int64_t>(t0) * p.q_stride * 2 +
                               static_cast<int64_t>(h0) * p.group * kRow;
     uint8_t* const o0 = reinterpret_cast<uint8_t*>(p.q_out) +
                         (static_cast<size_t>(t0) * p.num_kv_heads + h0) * p.group * kRow;
     const size_t o_stride = static_cast<size_t>(p.num_kv_heads) * p.group * kRow;
-    // SAME: the four rows belong to one token (its head count is a multiple of four): one address,
-    // one read of the angles.
-    auto q_stage = [&](int st, auto same_token) {
-      constexpr bool SAME = decltype(same_token)::value;
-      const int r0 = st * kStageRows + 4 * (lane >> 3);
-      if (r0 >= nq) return;
-      int ti = r0 / gq, hq = r0 - ti * gq;
-      uint4 a[4], b[4];
-      uint8_t* dst[4];
-      int tok[4];
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        tok[i] = SAME || r0 + i < nq ? ti : -1;
-        if (tok[i] < 0) continue;
-        const uint8_t* src = q0 + static_cast<int64_t>(ti) * p.q_stride * 2 + (SAME ? hq + i : hq) * kRow;
-        a[i] = ldg_stream(src + 16 * ca);
-        b[i] = ldg_stream(src + 16 * cb);
-        dst[i] = o0 + ti * o_stride + (SAME ? hq + i : hq) * kRow;
-        if (!SAME && ++hq == gq) {
-          hq = 0;
-          ti++;
-        }
-      }
-      f2 c[4], s[4];
-      int have = -1;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        if (!SAME && tok[i] < 0) continue;
-        if (turn && (SAME ? i == 0 : tok[i] != have)) {
-          have = tok[i];
-          const ulonglong2* src = reinterpret_cast<const ulonglong2*>(cs + have * kD + 8 * j);
-          const ulonglong2 c0 = src[0], c1 = src[1], s0 = src[kD / 8], s1 = src[kD / 8 + 1];
-          c[0] = c0.x, c[1] = c0.y, c[2] = c1.x, c[3] = c1.y;
-          s[0] = s0.x, s[1] = s0.y, s[2] = s1.x, s[3] = s1.y;
-        }
-        if (turn) {
-          rotate_chunks<BF16>(a[i], b[i], c, s, p.interleaved);
-        } else if (BF16) {  // unrotated channels: only the type changes
-          a[i] = half_chunk<BF16>(a[i]);
-          b[i] = half_chunk<BF16>(b[i]);
-        }
-        if (dest[tok[i]].slot == kSlotPadding) continue;
-        stg_128(dst[i] + 16 * ca, a[i].x, a[i].y, a[i].z, a[i].w);
-        stg_128(dst[i] + 16 * cb, b[i].x, b[i].y, b[i].z, b[i].w);
-      }
+    // The angles of token ti for this lane's pairs.
+    auto angles = [&](int ti, f2 (&c)[4], f2 (&s)[4]) {
+      const ulonglong2* src = reinterpret_cast<const ulonglong2*>(cs + ti * kD + 8 * j);
+      const ulonglong2 c0 = src[0], c1 = src[1], s0 = src[kD / 8], s1 = src[kD / 8 + 1];
+      c[0] = c0.x, c[1] = c0.y, c[2] = c1.x, c[3] = c1.y;
+      s[0] = s0.x, s[1] = s0.y, s[2] = s1.x, s[3] = s1.y;
     };
-    if ((gq & 3) == 0) {
-      for (int st = w; st < nsq; st += kWarps) q_stage(st, std::true_type{});
-    } else {
-      for (int st = w; st < nsq; st += kWarps) q_stage(st, std::false_type{});
+    // One row's chunks, rotated (or only converted: channels behind rotary_dim), stored to dst.
+    auto finish = [&](uint4& a, uint4& b, const f2 (&c)[4], const f2 (&s)[4], uint8_t* dst) {
+      if (turn) {
+        rotate_chunks<BF16, INTER>(a, b, c, s);
+      } else if (BF16) {
+        a = half_chunk<BF16>(a);
+        b = half_chunk<BF16>(b);
+      }
+      stg_128(dst + 16 * ca, a.x, a.y, a.z, a.w);
+      stg_128(dst + 16 * cb, b.x, b.y, b.z, b.w);
+    };
+    if ((gq & 3) == 0) {  // a lane's four rows belong to one token: one address, one read of its angles
+      for (int st = w; st < nsq; st += kWarps) {
+        const int r0 = st * kStageRows + 4 * (lane >> 3), ti = r0 / gq;
+        if (r0 >= nq) continue;
+        const uint8_t* const src = q0 + static_cast<int64_t>(ti) * p.q_stride * 2 + (r0 - ti * gq) * kRow;
+        uint8_t* const dst = o0 + ti * o_stride + (r0 - ti * gq) * kRow;
+        uint4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          a[i] = ldg_stream(src + i * kRow + 16 * ca);
+          b[i] = ldg_stream(src + i * kRow + 16 * cb);
+        }
+        f2 c[4], s[4];
+        angles(ti, c, s);
+        if (dest[ti].slot == kSlotPadding) continue;
+#pragma unroll
+        for (int i = 0; i < 4; i++) finish(a[i], b[i], c, s, dst + i * kRow);
+      }
+    } else {  // (few heads: a row at a time)
+#pragma unroll 1
+      for (int r = 4 * w + (lane >> 3); r < nq; r += 4 * kWarps) {
+        const int ti = r / gq;
+        const uint8_t* const src = q0 + static_cast<int64_t>(ti) * p.q_stride * 2 + (r - ti * gq) * kRow;
+        uint4 a = ldg_stream(src + 16 * ca), b = ldg_stream(src + 16 * cb);
+        f2 c[4], s[4];
+        angles(ti, c, s);
+        if (dest[ti].slot != kSlotPadding) finish(a, b, c, s, o0 + ti * o_stride + (r - ti * gq) * kRow);
+      }
     }
   }
 
@@ -394,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
     }
     if (active) {
       if (kind == 0) {
-        rope_row<BF16>(raw, row, cs_s + ti * (kD * 4), rho, l, p, x);
+        rope_row<BF16, INTER>(raw, row, cs_s + ti * (kD * 4), rho, l, p, x);
         first_stage<BLOCK>(x);
         rotate_stages<BLOCK>(rho, l, pmask, x);
       } else if constexpr (BF16) {
@@ -435,19 +429,26 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(RopeAppendPara
   }
 }
 
-template <int BLOCK, bool FP4, bool BF16>
+template <int BLOCK, bool FP4, bool BF16, bool INTER>
 int launch_one(const cudaLaunchConfig_t& cfg, const RopeAppendParams& p) {
-  if (!ensure_smem<rope_append_kernel<BLOCK, FP4, BF16>>(kMaxSmem)) return -2;
-  return cudaLaunchKernelEx(&cfg, rope_append_kernel<BLOCK, FP4, BF16>, p) == cudaSuccess ? 0 : -2;
+  if (!ensure_smem<rope_append_kernel<BLOCK, FP4, BF16, INTER>>(kMaxSmem)) return -2;
+  return cudaLaunchKernelEx(&cfg, rope_append_kernel<BLOCK, FP4, BF16, INTER>, p) == cudaSuccess ? 0 : -2;
 }
 
-template <bool FP4, bool BF16>
-int launch_block(const cudaLaunchConfig_t& cfg, const RopeAppendParams& p, int block) {
+template <int BLOCK, bool FP4>
+int launch_type(const cudaLaunchConfig_t& cfg, const RopeAppendParams& p, bool bf16) {
+  if (p.interleaved)
+    return bf16 ? launch_one<BLOCK, FP4, true, true>(cfg, p) : launch_one<BLOCK, FP4, false, true>(cfg, p);
+  return bf16 ? launch_one<BLOCK, FP4, true, false>(cfg, p) : launch_one<BLOCK, FP4, false, false>(cfg, p);
+}
+
+template <bool FP4>
+int launch_block(const cudaLaunchConfig_t& cfg, const RopeAppendParams& p, int block, bool bf16) {
   switch (block) {
-    case 1: return launch_one<1, FP4, BF16>(cfg, p);
-    case 32: return launch_one<32, FP4, BF16>(cfg, p);
-    case 64: return launch_one<64, FP4, BF16>(cfg, p);
-    case 128: return launch_one<128, FP4, BF16>(cfg, p);
+    case 1: return launch_type<1, FP4>(cfg, p, bf16);
+    case 32: return launch_type<32, FP4>(cfg, p, bf16);
+    case 64: return launch_type<64, FP4>(cfg, p, bf16);
+    case 128: return launch_type<128, FP4>(cfg, p, bf16);
     default: return -1;
   }
 }
@@ -481,8 +482,7 @@ int launch_rope_append(RopeAppendParams p, int block, bool fp4, bool bf16, int n
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (fp4) return bf16 ? launch_block<true, true>(cfg, p, block) : launch_block<true, false>(cfg, p, block);
-  return bf16 ? launch_block<false, true>(cfg, p, block) : launch_block<false, false>(cfg, p, block);
+  return fp4 ? launch_block<true>(cfg, p, block, bf16) : launch_block<false>(cfg, p, block, bf16);
 }
 
 }  // namespace kvq
