@@ -28,9 +28,9 @@
 // 20 passes over the keys).  The
 // pages are then written in ascending order from ballot masks.  A team of warps shares a query.
 //
-// Measured: 464 queries, 8 KV heads, G = 4, up to 1024 pages: 41 us in one wave of 264 CTAs, about
-// a quarter for q's codes, 0.4 for the scores and 0.3 for the choice, all of it dependency chains
-// (16 warps per SM at 128 registers, 42 % of the issue slots; the integer MMAs are busy for 17 %).
+// Measured: 464 queries, 8 KV heads, G = 4, up to 1024 pages: 37 us in one wave of 264 CTAs, about
+// a third each for q's codes, the scores and the choice, all of it dependency chains (16 warps per
+// SM at 128 registers, 43 % of the issue slots; the integer MMAs are busy for 20 %).
 // One decode step of 4 sequences of up to 2048 pages, 4 KV heads, G = 8: 12 us, of which the launch
 // and the memory round trips to the first page rows are half.
 //

@@ -21,12 +21,13 @@
 //      each computing both partners' products, cost 77).
 //   k, v: two lanes a row, as in the append kernel.  (Eight lanes a row straight from global memory
 //      repeat the scale's divisions and the addresses four times as often: 349 us against 303.)
-// Measured, 8 x 8192 tokens, 32 + 2 x 8 heads, INT4, b = 128: 274 us, 5.1 TB/s of algorithmic
-// bytes; 0.79 of the time that they take at the copy rate.  139 M warp instructions at 46 % of the
-// issue slots with 16 warps per SM (126 registers): memory latency at a tile's start and the
-// butterfly's dependency chains share the rest.  Not kept: one persistent CTA per slot with the
-// next tile's copies in flight (registers spill: 503 us); copies issued only after the tokens'
-// places are known (352 us).
+// Measured, 8 x 8192 tokens, 32 + 2 x 8 heads, INT4, b = 128: 262 us, 5.4 TB/s of algorithmic
+// bytes, 0.82 of the copy rate; 132 M warp instructions at 46 % of the issue slots with 16 warps per
+// SM.  One token for each of 16 sequences: 7.9 us, of which about 2 us are the chain of offsets,
+// length and page, and much of the rest instruction fetches: the form of the pairs is a template
+// parameter because the smaller code took 9.0 us down to 7.9 (and 274 to 262).  Not kept: one
+// persistent CTA per slot with the next tile's copies in flight (registers spill: 503 us); copies
+// issued only after the tokens' places are known (352 us); q rows loaded a stage ahead (266 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>

@@ -16,11 +16,11 @@
 // in the handle's scratch and the last to arrive merges them in the order of the parts, so the
 // result does not depend on the order of arrival.
 //
-// Measured: 16 sequences x 8 KV heads, G = 4, INT4, 4096 tokens each: 26 us, 2.7 TB/s (a plain
+// Measured: 16 sequences x 8 KV heads, G = 4, INT4, 4096 tokens each: 24.6 us, 2.8 TB/s (a plain
 // stream of these 69 MB takes 14 us; the dense decode of the same bytes 22.4 us); 951 queries x 4
-// KV heads, G = 8, NVFP4, 1024 tokens each: 204 us, 2.8 TB/s out of L2.  Bound by instructions:
-// about 560 a tile (INT4, G = 4) and 900 (NVFP4, G = 8), most of them dequantisation, at 47 and
-// 60 % of the issue slots; four CTAs per SM are 4 % faster than three with a deeper ring.
+// KV heads, G = 8, NVFP4, 1024 tokens each: 199 us, 2.8 TB/s out of L2.  Bound by instructions:
+// about 530 a tile (INT4, G = 4) and 870 (NVFP4, G = 8), most of them dequantisation, at 50 and
+// 62 % of the issue slots; four CTAs per SM are 4 % faster than three with a deeper ring.
 #include <cuda_fp16.h>
 #include <math_constants.h>
 #include <stdint.h>
