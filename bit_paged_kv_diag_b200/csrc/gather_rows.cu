@@ -21,7 +21,6 @@
 // (b = 64) 84 us, 5.0 TB/s -- 0.72 and 0.77 of the copy rate.  The arithmetic pipe is busy for 57 %
 // of the time, the issue slots for 65 %.  Stores straight from registers took 95 and 103 us, one of
 // K and V per warp 86 and 90 us.
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 

@@ -28,7 +28,6 @@
 // parameter because the smaller code took 9.0 us down to 7.9 (and 274 to 262).  Not kept: one
 // persistent CTA per slot with the next tile's copies in flight (registers spill: 503 us); copies
 // issued only after the tokens' places are known (352 us); q rows loaded a stage ahead (266 us).
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -57,7 +56,7 @@ struct TokenDest {
   int page;  // pool page, or -1
   int slot;  // slot of the page, or kSlotBadPos / kSlotPadding
   int pos;   // position of the angle
-  int pad;
+  int pad;   // (16 bytes)
 };
 
 __host__ __device__ inline int round16(int n) { return (n + 15) & ~15; }

@@ -59,8 +59,8 @@ struct UnitInfo {
   int h;
 };
 
-// This lane's page of tile x of the unit: its place in the list (page lane % kPPT of the tile) and
-// its first token in the page; negative: none.
+// This lane's page (lane % kPPT) of tile x of the unit: the logical page that the list names there;
+// negative: none.
 template <int SEFF>
 __device__ __forceinline__ int load_block(int x, int x1, int lane, const int32_t* list, const DecodeParams& p,
                                           const SparseParams& sp) {
