@@ -315,35 +315,74 @@ def decode_attention_noalloc(desc: Desc, pool, layer: int, q, seq_lens, page_tab
 class Rope:
     """The position rotation of :func:`rope_quant_append`: ``inv_freq`` fp32 CUDA
     [rotary_dim / 2] (kept alive here), channel pairs (i, i + rotary_dim / 2) or, interleaved,
-    (2i, 2i + 1); ``factor`` multiplies every cosine and sine."""
+    (2i, 2i + 1); ``factor`` multiplies every cosine and sine.  ``inv_freq`` may be set again (or
+    given other data in place) between calls; ``rotary_dim`` follows its length."""
 
     def __init__(self, inv_freq, interleaved=False, factor=1.0):
-        import torch
-        self._ptr = _dev_ptr(inv_freq, "inv_freq", torch.float32)  # checked once: the tensor is kept
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must have one dimension")
         self.inv_freq = inv_freq
-        self._device = inv_freq.get_device()
-        self.rotary_dim = 2 * int(inv_freq.shape[0])
         self.interleaved = bool(interleaved)
         self.factor = float(factor)
+
+    @property
+    def inv_freq(self):
+        return self._inv_freq
+
+    @inv_freq.setter
+    def inv_freq(self, t):
+        import torch
+        ptr = _dev_ptr(t, "inv_freq", torch.float32)
+        if t.dim() != 1:
+            raise ValueError("inv_freq must have one dimension")
+        self._inv_freq, self._ptr, self._device = t, ptr, t.get_device()
+        self.rotary_dim = 2 * int(t.shape[0])
+
+    def pointer(self, cache):
+        """Address of the frequencies for a call on ``cache``.  The tensor was checked when it was
+        set; it is checked again when its data has moved since."""
+        t = self._inv_freq
+        if t.data_ptr() != self._ptr:
+            self.inv_freq = t
+        if self.rotary_dim != 2 * t.numel():
+            raise ValueError(f"rotary_dim {self.rotary_dim} with {t.numel()} frequencies")
+        if self._device != cache.device:
+            raise ValueError(f"inv_freq must be on cuda:{cache.device}")
+        return self._ptr
 
 
 class BlockBounds:
     """Per-page key bounds of a cache, by pool page: ``codes`` int8 CUDA
     [num_layers][num_pages][num_kv_heads][2][128] (lower, then upper bounds) in units of
     ``scale`` fp32 [num_layers][num_pages][num_kv_heads].  Filled by
-    :func:`update_block_bounds`, read by :func:`select_blocks`."""
+    :func:`update_block_bounds`, read by :func:`select_blocks`.  Either may be set again to a tensor
+    that fits the other."""
 
     def __init__(self, codes, scale):
+        self._take(codes, scale)
+
+    def _take(self, codes, scale):
         import torch
-        self._ptrs = _dev_ptr(codes, "codes", torch.int8), _dev_ptr(scale, "scale", torch.float32)
+        ptrs = _dev_ptr(codes, "codes", torch.int8), _dev_ptr(scale, "scale", torch.float32)
         if tuple(codes.shape) != (*scale.shape, 2, 128) or scale.dim() != 3:
             raise ValueError("codes must be [layers][pages][heads][2][128], scale [layers][pages][heads]")
-        self.codes = codes  # (both are checked once and kept)
-        self.scale = scale
+        self._codes, self._scale, self._ptrs = codes, scale, ptrs
         self._shape = tuple(scale.shape)
         self._device = codes.get_device() if codes.get_device() == scale.get_device() else -1
+
+    @property
+    def codes(self):
+        return self._codes
+
+    @codes.setter
+    def codes(self, t):
+        self._take(t, self._scale)
+
+    @property
+    def scale(self):
+        return self._scale
+
+    @scale.setter
+    def scale(self, t):
+        self._take(self._codes, t)
 
     @classmethod
     def alloc(cls, cache):
@@ -354,6 +393,11 @@ class BlockBounds:
                    torch.zeros(*shape, dtype=torch.float32, device=dev))
 
     def pointers(self, cache):
+        """Addresses for a call on ``cache``.  Both tensors were checked when they were set; they
+        are checked again when their data has moved since."""
+        codes, scale = self._codes, self._scale
+        if (codes.data_ptr(), scale.data_ptr()) != self._ptrs:
+            self._take(codes, scale)
         if self._shape != cache.page_shape:
             raise ValueError(f"bounds of {self._shape} for a cache of {cache.page_shape}")
         if self._device != cache.device:
@@ -449,8 +493,7 @@ def rope_quant_append(cache: Cache, layer: int, k, v, cu_new_tokens, seq_lens, p
     vp, vs = _tokens(cache, v, "v", dtype, (T, cache.kv_heads, 128))
     batch, sl, pt, cu = _seqs(cache, seq_lens, page_table, cu_new_tokens, "cu_new_tokens")
     pos = None if positions is None else _arg(cache, positions, "positions", _torch.int32, (T,))
-    if rope._device != cache.device:
-        raise ValueError(f"inv_freq must be on cuda:{cache.device}")
+    freq = rope.pointer(cache)
     qp, qs, op = None, 0, None
     if q is not None:
         shape = (T, cache.q_heads, 128)
@@ -463,7 +506,7 @@ def rope_quant_append(cache: Cache, layer: int, k, v, cu_new_tokens, seq_lens, p
     elif q_out is not None:
         raise ValueError("q_out without q")
     _run(cache, stream, "kvq_rope_quant_append", int(layer), code, qp, qs, kp, ks, vp, vs, cu, sl, pos, pt,
-         batch, T, rope._ptr, rope.rotary_dim, int(rope.interleaved), rope.factor, op)
+         batch, T, freq, rope.rotary_dim, int(rope.interleaved), rope.factor, op)
     return q_out
 
 
