@@ -1,4 +1,5 @@
 """Calls around the cache that the documentation allows and that are easily answered wrongly (GPU)."""
+import pytest
 
 from test_sparse_ops_gpu import D, Setup
 
