@@ -147,8 +147,8 @@ __device__ __forceinline__ Dest pair_dest(const AppendParams& p, int gp, uint32_
 
 template <int BLOCK, bool FP4>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kernel(AppendParams p) {
-  // The next kernel may start its own prologue; the pool stores below wait for every
-  // earlier kernel (griddep_wait), so they never race with a decode still reading.
+  // The next kernel may start its own prologue; the row copies and the pool stores below wait
+  // for every earlier kernel (griddep_wait): it may be writing these rows or reading the pool.
   griddep_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kernel(AppendPara
 #pragma unroll
     for (int s = 0; s < kStages; s++) mbar_init(bar0 + 8 * s, 1);
     fence_mbar_init();
+    griddep_wait();  // (the other lanes: before their first store)
 #pragma unroll
     for (int s = 0; s < kStages; s++) {
       const int j = gw + s * W;

@@ -325,8 +325,15 @@ struct NewRow {
   uint32_t scale;    // fp16 bits, same in every lane
 };
 
+// Channels 4*lane..4*lane+3 of a row that another kernel may still be writing (a load before
+// the wait): each word is one that was there, and a later load is not served from this one's line.
 __device__ __forceinline__ uint2 load_new_row(const __half* row, int lane) {
-  return __ldg(reinterpret_cast<const uint2*>(row) + lane);  // channels 4*lane..4*lane+3
+  uint2 r;
+  asm volatile("ld.relaxed.gpu.global.v2.u32 {%0,%1}, [%2];"
+               : "=r"(r.x), "=r"(r.y)
+               : "l"(reinterpret_cast<const uint2*>(row) + lane)
+               : "memory");
+  return r;
 }
 
 // The rotated row y = fl(c_b * butterfly(x)) of channels 4*lane..4*lane+3.
@@ -534,8 +541,8 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
   const int cap = p.max_pages_per_seq * p.page_size;
   // The prologue below reads only seq_lens and the page table, which no kernel of this
   // library writes (and may OR bits into the status word); everything else an earlier
-  // kernel may write or read (pool, q, new K/V rows, out, the scratch) is touched only
-  // after griddep_wait().
+  // kernel may write or read (pool, q, out, the scratch) is touched only after
+  // griddep_wait(), and the new K/V rows are what they are after it.
   griddep_launch_dependents();
 
   const uint32_t qbar_cta = smem_addr(bars + kWarps * (kStages + 1));
@@ -638,25 +645,37 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
 
   // Fused append: if this warp holds the last tile of its first unit and that unit's q
   // comes from a CTA table (its own fragment table is then free as the patch buffer), the
-  // unit's new K/V rows are loaded, rotated and quantised before the wait -- the inputs
-  // of an append are complete when the previous kernel lets this one start, and this is
-  // pure arithmetic into shared memory; the pool store waits.  Other units do it at their
-  // segment's start.
+  // unit's new K/V rows are loaded, rotated and quantised before the wait: pure arithmetic
+  // into shared memory, under the previous kernel's tail.  That kernel may be the one that
+  // writes these rows, so they are read again after the wait, and quantised again if they
+  // are not the same.  Other units do all of it at their segment's start.
   bool pre_quantised = false;
+  uint2 kraw0 = make_uint2(0u, 0u), vraw0 = make_uint2(0u, 0u);
+  auto new_row = [&](const __half* rows) {
+    return load_new_row(rows + (static_cast<size_t>(cu.b) * p.num_kv_heads + cu.h) * kD, lane);
+  };
   if constexpr (FUSED) {
     if (x < X1 && (is_uf(cu) || is_ul(cu))) {
       const int seg_end0 = min(X1, cu.U + cu.n);
       const int xl0 = x + kWarps * ((seg_end0 - x + kWarps - 1) / kWarps - 1);
       if (xl0 == cu.U + cu.n - 1) {
-        const size_t row = (static_cast<size_t>(cu.b) * p.num_kv_heads + cu.h) * kD;
-        fused_quantise<FP4>(load_new_row(p.k_new + row, lane), load_new_row(p.v_new + row, lane), lane,
-                            reinterpret_cast<uint8_t*>(frag), p);
+        kraw0 = new_row(p.k_new);
+        vraw0 = new_row(p.v_new);
+        fused_quantise<FP4>(kraw0, vraw0, lane, reinterpret_cast<uint8_t*>(frag), p);
         pre_quantised = true;
       }
     }
   }
 
   griddep_wait();
+
+  uint2 kraw1 = kraw0, vraw1 = vraw0;
+  if constexpr (FUSED) {
+    if (pre_quantised) {  // (the same in the whole warp)
+      kraw1 = new_row(p.k_new);
+      vraw1 = new_row(p.v_new);
+    }
+  }
 
   // q goes ahead of the tile copies, so that it is not queued behind them; then the first
   // kStages tiles.
@@ -708,6 +727,11 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
                              sf_all + (kWarps + t) * 8, lane, p, w);
   if (dead && lane == 0) atomicOr(p.status, KVQ_DEV_TIMEOUT_BIT);
   __syncthreads();
+  if constexpr (FUSED) {
+    if (pre_quantised &&
+        __any_sync(kFull, kraw0.x != kraw1.x || kraw0.y != kraw1.y || vraw0.x != vraw1.x || vraw0.y != vraw1.y))
+      fused_quantise<FP4>(kraw1, vraw1, lane, reinterpret_cast<uint8_t*>(frag), p);
+  }
   State<G> st;
   state_reset<G>(st);
   typename QF<G, FP4>::type qf;
@@ -741,11 +765,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
       const int xl = x + kWarps * (nt - 1);  // this warp's last tile of the unit
       uint8_t* patch = reinterpret_cast<uint8_t*>(frag);  // free until the next unit's q
       if (xl == cu.U + cu.n - 1 && !dead) {
-        if (!(pre_quantised && x == X0 + w)) {
-          const size_t row = (static_cast<size_t>(cu.b) * p.num_kv_heads + cu.h) * kD;
-          fused_quantise<FP4>(load_new_row(p.k_new + row, lane), load_new_row(p.v_new + row, lane), lane,
-                              patch, p);
-        }
+        if (!(pre_quantised && x == X0 + w)) fused_quantise<FP4>(new_row(p.k_new), new_row(p.v_new), lane, patch, p);
         new_ok = fused_store<FP4>(cu.b, cu.h, lane, patch, p);
         if (lane == 0)
           *reinterpret_cast<int*>(patch + PatchLayout<FP4>::kJ) = cu.L - 1 - (xl - cu.U) * kTileTokens;

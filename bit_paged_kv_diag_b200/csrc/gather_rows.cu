@@ -211,8 +211,7 @@ __device__ __forceinline__ void row_fp4(const uint32_t (&w)[8], uint32_t sc, flo
 template <int BLOCK, bool FP4, bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) gather_kernel(GatherParams p) {
   __shared__ __align__(128) uint8_t stage[kWarps][2][kRowsPerWarp * kRowStride];
-  // (No early launch of the next kernel: it may be an append that takes these rows as its k and v,
-  // which it reads before it waits.)
+  griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, l = lane & 1;
   const unsigned pmask = 0x3u << (lane & 30);

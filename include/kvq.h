@@ -68,17 +68,16 @@
  *     (decode calls share the handle's scratch).
  *   * Launch overlap: every kernel of this library uses programmatic dependent launch.  Each lets the next
  *     kernel on the stream start at its own entry, and waits for the previous kernel to
- *     complete before it touches the pool, q, out or the handle's scratch.  Before that
- *     wait, decode already reads seq_lens and page_table, append reads k, v,
- *     cu_new_tokens, seq_lens and page_table, and the fused append + decode reads k_new,
- *     v_new, seq_lens and page_table, and prefill attention reads cu_q, seq_lens and
- *     page_table.  These arrays must therefore be complete
- *     when the previous kernel on the stream lets its dependents start.  Kernels that do
- *     not use programmatic launch (PyTorch's, cuBLAS's, copies) only do so by completing,
- *     and this library's own kernels never write these arrays.  The calls from
- *     kvq_rope_quant_append to kvq_sparse_attention wait before they read anything, and
- *     kvq_gather_rows, whose outputs may be an append's k and v, completes before the next
- *     kernel starts.
+ *     complete before it touches the pool, q, k, v, out or the handle's scratch: any output
+ *     of one call may be the q, k or v of the next.  Before that wait, decode and the fused
+ *     append + decode already read seq_lens and page_table, append reads cu_new_tokens,
+ *     seq_lens and page_table, and prefill attention reads cu_q, seq_lens and page_table.
+ *     These arrays must therefore be complete when the previous kernel on the stream lets
+ *     its dependents start.  Kernels that do not use programmatic launch (PyTorch's,
+ *     cuBLAS's, copies) only do so by completing, and this library's own kernels never write
+ *     these arrays.  The calls from kvq_rope_quant_append to kvq_sparse_attention wait before
+ *     they read anything.  (The fused append + decode looks at k_new and v_new early, and
+ *     again after the wait; only what it finds then counts.)
  *   * The current device must be the one the handle was made on; the calls from
  *     kvq_rope_quant_append to kvq_sparse_attention return KVQ_EINVAL otherwise.
  */

@@ -31,3 +31,52 @@ def test_tensors_set_again_between_calls():
         assert torch.equal(got_q, want_q) and torch.equal(s.pool, want)
         assert torch.equal(bounds.codes, fresh.codes) and torch.equal(bounds.scale, fresh.scale)
     assert s.status() == 0
+
+
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_outputs_of_a_call_feed_an_append(fused, fmt):
+    """q' of the rotating append, attention outputs and rows read back are the k and v of an append
+    or of a fused step that follows at once on the stream."""
+    import torch
+    B, hkv = 6, 4
+    n = 1 if fused else 700
+    s = Setup([900, 40, 0, 333, 2000, 17], [n] * B, hkv, 1, 64, 64, fmt, layers=2, layer=0).fill()
+    kvq, cu, lens, after = s.kvq, s.dev(s.cu), s.dev(s.before), s.dev(s.after)
+    x, y = (torch.randn(s.T, hkv, D, device="cuda").half() for _ in range(2))
+    rope = kvq.Rope((1e4 ** -(torch.arange(0, 128, 2, device="cuda") / 128)).float())
+    blocks = torch.zeros(s.T, hkv, 8, dtype=torch.int32, device="cuda")
+    blocks[:] = torch.arange(8, dtype=torch.int32, device="cuda")
+    k, v, q = torch.empty_like(x), torch.empty_like(x), torch.ones(B, hkv, D, device="cuda").half()
+    out = torch.empty_like(q)
+
+    def rotated():
+        kvq.rope_quant_append(s.cache, 0, x, y, cu, lens, s.pt, rope, q=x, q_out=k)
+        v.copy_(y)
+        kvq.rope_quant_append(s.cache, 0, x, y, cu, lens, s.pt, rope, q=y, q_out=v)
+
+    def attended():
+        kvq.sparse_attention(s.cache, 0, x, after, s.pt, blocks, cu_q=cu, out=k)
+        kvq.prefill_attention(s.cache, 0, y, cu, after, s.pt, out=v)
+
+    def read_back():
+        kvq.gather_rows(s.cache, 0, cu, lens, s.pt, s.T, k_out=k, v_out=v)
+
+    def append():
+        if fused:
+            kvq.append_decode_attention(s.cache, 1, k, v, q, lens, s.pt, out=out)
+        else:
+            kvq.rotate_quant_append(s.cache, 1, k, v, cu, lens, s.pt)
+
+    for make in (rotated, attended, read_back):
+        got = []
+        for wait in (False, False, True):
+            k.zero_(), v.zero_(), s.pool[s.pool.numel() // 2:].zero_()
+            make()
+            if wait:
+                torch.cuda.synchronize()
+            append()
+            got.append((s.pool.clone(), out.clone()))
+        for pool, o in got[:2]:
+            assert torch.equal(pool, got[2][0]) and (not fused or torch.equal(o, got[2][1])), make.__name__
+    assert s.status() == 0
