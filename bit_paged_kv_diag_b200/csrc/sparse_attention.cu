@@ -167,18 +167,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
   const int xl = x0 + w + kWarps * (lane / kPPT);  // this lane's tile of the first batch
   const int blk0 = load_block<SEFF>(xl, x1, lane, list, p, sp);
 
-  // The query's sequence and position.
-  int b = t, pos;
+  // The query's sequence and position.  A sequence is good or bad as a whole: every row of one that
+  // is shorter than its chunk or does not fit its table is zeros.
+  int b = t, len, pos, fewest = 0;
   if (sp.cu_q) {
     int first, end;
     const SeqWindow win = seq_window(sp.cu_q, p.batch, t);
     b = seq_find(win, sp.cu_q, p.batch, t, first, end);
     if (t < first || t >= end) return;  // a row of no sequence: left as it is
-    pos = __ldg(p.seq_lens + b) - (end - t);
+    len = __ldg(p.seq_lens + b);
+    pos = len - (end - t);
+    fewest = end - first;
   } else {
-    pos = __ldg(p.seq_lens + b) - 1;
+    len = __ldg(p.seq_lens + b);
+    pos = len - 1;
   }
-  if (pos < (sp.cu_q ? 0 : -1) || pos >= p.max_pages_per_seq * p.page_size) {
+  if (len < fewest || len > static_cast<long long>(p.max_pages_per_seq) * p.page_size) {
     if (tid == 0) atomicOr(p.status, KVQ_DEV_BAD_POS_BIT);
     pos = -1;
   }

@@ -1,4 +1,5 @@
 """Calls around the cache that the documentation allows and that are easily answered wrongly (GPU)."""
+import numpy as np
 import pytest
 
 from test_sparse_ops_gpu import D, Setup
@@ -80,3 +81,31 @@ def test_outputs_of_a_call_feed_an_append(fused, fmt):
         for pool, o in got[:2]:
             assert torch.equal(pool, got[2][0]) and (not fused or torch.equal(o, got[2][1])), make.__name__
     assert s.status() == 0
+
+
+@pytest.mark.parametrize("group,page", [(1, 16), (4, 64)])
+def test_rows_of_a_bad_sequence_are_zeros(group, page):
+    """A sequence shorter than its chunk, longer than its table or of a negative length: all of its
+    rows are zeros, whatever their own positions and lists; the others' are what they are without it."""
+    import torch
+    s = Setup([30, 30, 30, 30, 30], [3, 4, 3, 3, 2], 2, group, 64, page, 0).fill()
+    kvq, cap = s.kvq, s.width * page
+    cu, q = s.dev(s.cu), torch.randn(s.T, s.hq, D, device="cuda").half()
+    blocks = torch.zeros(s.T, s.hkv, 2, dtype=torch.int32, device="cuda")
+    blocks[:, :, 1] = 1
+    want = kvq.sparse_attention(s.cache, 0, q, s.dev(s.after), s.pt, blocks, cu_q=cu)
+    assert s.status() == 0 and want.any(-1).all()
+    lens = s.after.copy()
+    lens[0], lens[1], lens[3] = 2, cap + 2, -1  # (2: a row of it has a position; cap + 2: two rows are inside)
+    bad = np.isin(s.seq, (0, 1, 3))
+    out = kvq.sparse_attention(s.cache, 0, q, s.dev(lens), s.pt, blocks, cu_q=cu).cpu()
+    assert s.status() == kvq.KVQ_DEV_BAD_POS
+    assert not out[bad].any() and torch.equal(out[~bad], want.cpu()[~bad])
+    # One query per sequence: an empty sequence is not a bad one.
+    lens = np.array([0, cap + 1, -5, cap, 1], np.int32)
+    full = np.array([33, 33, 33, cap, 1], np.int32)
+    want = kvq.sparse_attention(s.cache, 0, q[:5].contiguous(), s.dev(full), s.pt, blocks[:5].contiguous()).cpu()
+    assert s.status() == 0
+    out = kvq.sparse_attention(s.cache, 0, q[:5].contiguous(), s.dev(lens), s.pt, blocks[:5].contiguous()).cpu()
+    assert s.status() == kvq.KVQ_DEV_BAD_POS
+    assert not out[:3].any() and torch.equal(out[3:], want[3:]) and out[3:].any(-1).all()
