@@ -200,15 +200,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kernel(AppendPara
     Dest dnext = {-1, -1, 0};
     if (j + W < nws && gp + W * kPairs < npairs) dnext = pair_dest(p, gp + W * kPairs, cursor);
 
-    if (!mbar_wait_bounded(bar0 + 8 * s, phase, kWaitLimitNs)) {
-      // A copy did not land in time: flag it, let this warp's other copies finish
-      // (bounded) so nothing lands in shared memory after the CTA exits, and stop.
+    if (!mbar_wait_warp(bar0 + 8 * s, phase, kWaitLimitNs)) {
+      // A copy did not land in time: flag it, give it and this warp's other copies another
+      // (bounded) wait so that nothing lands in shared memory after the CTA exits, and stop.
       if (lane == 0) atomicOr(p.status, KVQ_DEV_TIMEOUT_BIT);
 #pragma unroll
-      for (int k = 1; k < kStages; k++) {
+      for (int k = 0; k < kStages; k++) {
         const int sk = (s + k) % kStages;
         if (j + k * W < nws)
-          mbar_wait_bounded(bar0 + 8 * sk, sk > s ? phase : phase ^ 1u, kWaitLimitNs);
+          mbar_wait_warp(bar0 + 8 * sk, sk >= s ? phase : phase ^ 1u, kWaitLimitNs);
       }
       return;
     }

@@ -130,12 +130,13 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(BoundsParams p) {
     hx[e] = 0xFC00FC00u;
     hn[e] = 0x7C007C00u;
   }
-  bool dead = false;
   for (int q = 0; q * kRows < filled; q++) {
-    if (!mbar_wait_bounded(bar + 8 * (q & 1), (q >> 1) & 1, kWaitLimitNs)) {
-      dead = true;
-      if ((q + 1) * kRows < filled) mbar_wait_bounded(bar + 8 * ((q + 1) & 1), ((q + 1) >> 1) & 1, kWaitLimitNs);
-      break;
+    if (!mbar_wait_warp(bar + 8 * (q & 1), (q >> 1) & 1, kWaitLimitNs)) {
+      // Flag it and let the copies in flight land (bounded) before their memory is reused.
+      if (lane == 0) atomicOr(p.status, KVQ_DEV_TIMEOUT_BIT);
+      mbar_wait_warp(bar + 8 * (q & 1), (q >> 1) & 1, kWaitLimitNs);
+      if ((q + 1) * kRows < filled) mbar_wait_warp(bar + 8 * ((q + 1) & 1), ((q + 1) >> 1) & 1, kWaitLimitNs);
+      return;
     }
     const uint8_t* slot = ring[w][q & 1];
     const uint32_t* codes = reinterpret_cast<const uint32_t*>(slot) + j8;
@@ -194,10 +195,6 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(BoundsParams p) {
       fence_proxy_async_smem();
       fetch(q + 2);
     }
-  }
-  if (__any_sync(0xffffffffu, dead)) {
-    if (lane == 0) atomicOr(p.status, KVQ_DEV_TIMEOUT_BIT);
-    return;
   }
   if constexpr (FP4) {
 #pragma unroll

@@ -720,13 +720,13 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
   int consumed = 0;   // tiles of this warp consumed (tile t uses slot t % kStages)
   bool dead = false;  // a bounded wait gave up: stop touching the ring
   // uf's and ul's q rows: every warp rotates and slices its share of the queries.
-  if (!mbar_wait_bounded(qbar_cta, 0u, kWaitLimitNs)) dead = true;
-  if (!dead)
-    for (int t = 0; t < (two_edges ? 2 : 1); t++)
-      prep_q<G, kWarps, FP4>(qraw_all + (kWarps + t) * G * kD * 2, frag_all + (kWarps + t) * kFragWords,
-                             sf_all + (kWarps + t) * 8, lane, p, w);
+  // (A wait that gave up joins the CTA at the barrier; until then it works on whatever is there.)
+  const bool q_late = !mbar_wait_bounded(qbar_cta, 0u, kWaitLimitNs);
+  for (int t = 0; t < (two_edges ? 2 : 1); t++)
+    prep_q<G, kWarps, FP4>(qraw_all + (kWarps + t) * G * kD * 2, frag_all + (kWarps + t) * kFragWords,
+                           sf_all + (kWarps + t) * 8, lane, p, w);
+  dead = __syncthreads_or(q_late);
   if (dead && lane == 0) atomicOr(p.status, KVQ_DEV_TIMEOUT_BIT);
-  __syncthreads();
   if constexpr (FUSED) {
     if (pre_quantised &&
         __any_sync(kFull, kraw0.x != kraw1.x || kraw0.y != kraw1.y || vraw0.x != vraw1.x || vraw0.y != vraw1.y))
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
       qfrag_get<G>(qf, frag_all + table * kFragWords, sf_all + table * 8, lane);
     } else {
       if (!dead) {
-        if (mbar_wait_bounded(qbar, static_cast<uint32_t>(q_done & 1), kWaitLimitNs)) q_done++;
+        if (mbar_wait_warp(qbar, static_cast<uint32_t>(q_done & 1), kWaitLimitNs)) q_done++;
         else dead = true;
       }
       if (!dead) prep_q<G, 1, FP4>(qraw, frag, sf, lane, p);
@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
     int slot_i = consumed % kStages;
     uint32_t parity = static_cast<uint32_t>((consumed / kStages) & 1);
     if (!dead) {
-      if (!mbar_wait_bounded(bar_s + 8 * slot_i, parity, kWaitLimitNs)) {
+      if (!mbar_wait_warp(bar_s + 8 * slot_i, parity, kWaitLimitNs)) {
         dead = true;
       } else {
         if constexpr (FUSED) {
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
       const int cur = slot_i;
       const int nslot = cur + 1 == kStages ? 0 : cur + 1;
       const uint32_t npar = cur + 1 == kStages ? parity ^ 1u : parity;
-      if (!mbar_wait_bounded(bar_s + 8 * nslot, npar, kWaitLimitNs)) {
+      if (!mbar_wait_warp(bar_s + 8 * nslot, npar, kWaitLimitNs)) {
         dead = true;
         break;
       }
@@ -925,11 +925,11 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
   if (dead) {
     // Let copies still in flight land before the CTA's shared memory is released.
     for (int j = consumed; j < pr.t; j++)
-      mbar_wait_bounded(bar_s + 8 * (j % kStages), static_cast<uint32_t>((j / kStages) & 1),
+      mbar_wait_warp(bar_s + 8 * (j % kStages), static_cast<uint32_t>((j / kStages) & 1),
                         kWaitLimitNs);
     for (; q_done < q_issued; q_done++)
-      mbar_wait_bounded(qbar, static_cast<uint32_t>(q_done & 1), kWaitLimitNs);
-    mbar_wait_bounded(qbar_cta, 0u, kWaitLimitNs);
+      mbar_wait_warp(qbar, static_cast<uint32_t>(q_done & 1), kWaitLimitNs);
+    mbar_wait_warp(qbar_cta, 0u, kWaitLimitNs);
   }
 }
 

@@ -89,7 +89,9 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 
 // Wait for phase `parity` of a barrier, giving up after `limit_ns` nanoseconds.
 // Returns false on timeout (the caller records KVQ_DEV_TIMEOUT and stops using the
-// slot); never spins forever.
+// slot); never spins forever.  Every lane has its own clock, so lanes of a warp may get
+// different answers: a warp that goes another way after a timeout (past its barriers,
+// shuffles and votes) takes mbar_wait_warp.
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
                                                   uint64_t limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -97,6 +99,19 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+
+// The same by a whole warp, with one answer for all lanes: one vote when the phase is complete, as it
+// mostly is; otherwise the lanes go on until all have seen it or one's time is up.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (!ok) ok = mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > limit_ns)) return false;
   }
 }
 

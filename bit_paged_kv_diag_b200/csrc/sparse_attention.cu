@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
     else return Valid{{v.x, v.y}};
   };
   if (issued > 0) {
-    if (!mbar_wait_bounded(bar_s, 0u, kWaitLimitNs)) {
+    if (!mbar_wait_warp(bar_s, 0u, kWaitLimitNs)) {
       dead = true;
     } else {
       tile_qk_any<G, SEFF>(qf, ring_w, valid_of(0), lane, sc);
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
   while (consumed + 1 < issued && !dead) {
     const int cs = slot_i, ns = cs + 1 == kRing<FP4> ? 0 : cs + 1;
     const uint32_t npar = cs + 1 == kRing<FP4> ? parity ^ 1u : parity;
-    if (!mbar_wait_bounded(bar_s + 8 * ns, npar, kWaitLimitNs)) {
+    if (!mbar_wait_warp(bar_s + 8 * ns, npar, kWaitLimitNs)) {
       dead = true;
       break;
     }
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) sparse_kernel(DecodePara
     // Flag it and let the copies still in flight land (bounded) before their memory is reused.
     if (lane == 0) atomicOr(p.status, KVQ_DEV_TIMEOUT_BIT);
     for (int j = consumed; j < issued; j++)
-      mbar_wait_bounded(bar_s + 8 * (j % kRing<FP4>), static_cast<uint32_t>((j / kRing<FP4>) & 1), kWaitLimitNs);
+      mbar_wait_warp(bar_s + 8 * (j % kRing<FP4>), static_cast<uint32_t>((j / kRing<FP4>) & 1), kWaitLimitNs);
   }
   // The warps' records, each in its own drained ring; an idle warp's has m = -inf, l = 0.
   __syncwarp();
