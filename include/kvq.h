@@ -67,8 +67,8 @@
  *     pool when it allocated it.  One handle must not be used from two streams at once
  *     (decode calls share the handle's scratch).
  *   * Launch overlap: every kernel of this library uses programmatic dependent launch.  Each lets the next
- *     kernel on the stream start at its own entry, and waits for the previous kernel to
- *     complete before it touches the pool, q, k, v, out or the handle's scratch: any output
+ *     kernel on the stream start at its own entry (kvq_gather_rows: when its blocks end), and
+ *     waits for the previous kernel to complete before it touches the pool, q, k, v, out or the handle's scratch: any output
  *     of one call may be the q, k or v of the next.  Before that wait, decode and the fused
  *     append + decode already read seq_lens and page_table, append reads cu_new_tokens,
  *     seq_lens and page_table, and prefill attention reads cu_q, seq_lens and page_table.
