@@ -465,10 +465,12 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
       }
     };
     // Taken: the pages that always are, the keys >= T, and the first `quota` keys equal to T - 1.
+    // (Of a query without a score every key may be the largest integer, NaN's: T is then 0, one
+    // more than it, and no key is above.)
     uint32_t T = 0xFFFFFFFFu;
     int quota = 0;
-    int need = k - p.sink - p.recent;  // >= 0 (host-checked), < the keys that are a choice
-    const bool need_any = need > 0;
+    const int chosen = k - p.sink - p.recent;  // >= 0 (host-checked), < the keys that are a choice
+    int need = chosen;
     if (need > 0) {
       uint32_t lo = 0xFFFFFFFFu, hi = 0u;
       each4([&](uint4 v) {
@@ -568,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
         }
       }
     }
+    const bool any_above = chosen > 0 && T != 0u;
     // The pages in ascending order: each warp of the team a contiguous part; lane i of a warp
     // holds the mask of the part's pages 32 i .. 32 i + 31.
     const int words = (np + 31) / 32, per = (words + TW - 1) / TW;
@@ -585,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(SelectParams p) {
 #pragma unroll 8
       for (int i = 0; i < m; i++) {
         const uint32_t key = kq[(base + i) * 32 + lane];
-        const uint32_t ms = __ballot_sync(kFull, key >= T && need_any);
+        const uint32_t ms = __ballot_sync(kFull, key >= T && any_above);
         if (lane == i) sure = ms;
       }
       sure |= forced;

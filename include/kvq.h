@@ -336,7 +336,8 @@ KVQ_API int kvq_update_block_bounds(kvq_cache* c, int32_t layer, void* codes, fl
  *   score = max over the KV head's query heads g of fl32(I_g s_g) * sigma,
  *   I_g = sum_d max(c_d, 0) hi_d + min(c_d, 0) lo_d,
  * where c = rint(y / s), s = fl32(max |y| / 127), y = q rotated with the cache's transform; a
- * tie goes to the lower page.
+ * tie goes to the lower page.  (A head with a NaN does not count; where every head has one, the
+ * others are all tied.)
  *   codes, scale   as kvq_update_block_bounds left them
  *   q              device fp16 [total_q][num_q_heads][128], 16-byte aligned (q' of
  *                  kvq_rope_quant_append)

@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from test_sparse_ops_gpu import D, Setup
+from test_sparse_ops_gpu import D, Setup, _filled_bounds
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +109,31 @@ def test_rows_of_a_bad_sequence_are_zeros(group, page):
     out = kvq.sparse_attention(s.cache, 0, q[:5].contiguous(), s.dev(lens), s.pt, blocks[:5].contiguous()).cpu()
     assert s.status() == kvq.KVQ_DEV_BAD_POS
     assert not out[:3].any() and torch.equal(out[3:], want[3:]) and out[3:].any(-1).all()
+
+
+@pytest.mark.parametrize("hkv,group,before,new,chunk", [
+    (1, 1, [4000, 900], [1, 1], False), (2, 4, [4000, 900], [1, 1], False), (1, 8, [30000], [1], False),
+    (2, 2, [4000, 900], [20, 30], True), (1, 4, [600], [5], True)])
+def test_queries_without_a_score_keep_the_first_and_last_pages(hkv, group, before, new, chunk):
+    """No score of a query with a NaN in every head is a number: its pages are the first, the last
+    and, all others being equal, the lowest.  The other queries' do not change."""
+    import torch
+    s = Setup(before, new, hkv, group, 64, 16, 0).fill()
+    bounds, *_ = _filled_bounds(s, s.host())
+    q = torch.randn(s.T, s.hq, D, device="cuda").half()
+
+    def choose(q):
+        return s.kvq.select_blocks(s.cache, 0, q, s.dev(s.after), s.pt, bounds, 10, cu_q=s.dev(s.cu) if chunk else None,
+                                   sink=2, recent=3).cpu().numpy()
+
+    want, nan = choose(q), np.arange(s.T) % 3 == 0
+    bad = q.clone()
+    bad[torch.from_numpy(nan).cuda(), :, 17] = float("nan")
+    got = choose(bad)
+    for t in range(s.T):
+        n = int(s.pos[t]) // 16 + 1
+        if nan[t]:
+            assert (got[t] == [0, 1, 2, 3, 4, 5, 6, n - 3, n - 2, n - 1]).all(), (t, got[t])
+        else:
+            assert np.array_equal(got[t], want[t])
+    assert s.status() == 0
