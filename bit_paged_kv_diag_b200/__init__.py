@@ -386,7 +386,7 @@ class BlockBounds:
 
     @classmethod
     def alloc(cls, cache):
-        """Bounds for every page of ``cache`` (264 bytes per page, KV head and layer)."""
+        """Bounds for every page of ``cache`` (260 bytes per page, KV head and layer)."""
         import torch
         shape, dev = cache.page_shape, cache.torch_device
         return cls(torch.zeros(*shape, 2, 128, dtype=torch.int8, device=dev),

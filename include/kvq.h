@@ -350,7 +350,7 @@ KVQ_API int kvq_update_block_bounds(kvq_cache* c, int32_t layer, void* codes, fl
  *                  (position / page_size) in ascending order, then -1
  * A sequence shorter than its chunk or beyond its page budget is flagged and its rows are -1;
  * rows behind cu_q[batch] are left as they were; a bad page is flagged and scores 0.
- * max_pages_per_seq up to 49,920 (the scores of a query stay in shared memory):
+ * max_pages_per_seq up to 50,048 (the scores of a query stay in shared memory):
  * KVQ_EUNSUPPORTED beyond. */
 KVQ_API int kvq_select_blocks(kvq_cache* c, int32_t layer, const void* codes,
                               const float* scale, const void* q, const int32_t* cu_q,

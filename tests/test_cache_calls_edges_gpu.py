@@ -137,3 +137,28 @@ def test_queries_without_a_score_keep_the_first_and_last_pages(hkv, group, befor
         else:
             assert np.array_equal(got[t], want[t])
     assert s.status() == 0
+
+
+def test_widest_page_table():
+    """The last accepted width of a page table chooses as an exact one does; the next is refused."""
+    import torch
+    widest = 50048
+    s = Setup([3000], [1], 1, 4, 64, 16, 0).fill()
+    bounds, *_ = _filled_bounds(s, s.host())
+    q, after = torch.randn(1, 4, D, device="cuda").half(), s.dev(s.after)
+    want = s.kvq.select_blocks(s.cache, 0, q, after, s.pt, bounds, 9)
+    for width in (widest, widest + 1):
+        d = s.kvq.Desc(1, 1, 4, D, 64, 16, s.pages, 1, width, 0)
+        cache, _ = s.kvq.alloc_pages(d, pool=s.pool)
+        table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+        table[:, :s.width] = s.pt
+        if width == widest:
+            assert torch.equal(s.kvq.select_blocks(cache, 0, q, after, table, bounds, 9), want)
+            cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+            assert torch.equal(s.kvq.select_blocks(cache, 0, q, after, table, bounds, 9, cu_q=cu), want)
+        else:
+            with pytest.raises(s.kvq.KVQError) as e:
+                s.kvq.select_blocks(cache, 0, q, after, table, bounds, 9)
+            assert e.value.status == s.kvq.KVQ_EUNSUPPORTED
+        assert s.kvq.get_device_status(cache) == 0
+        cache.close()

@@ -103,3 +103,26 @@ def test_bounds_that_do_not_fit_are_refused(calls):
     with pytest.raises(ValueError):
         _bounds(cache, bounds)
     assert len(seen) == 1
+
+
+def test_bytes_of_the_bounds():
+    """What BlockBounds.alloc says that a page, KV head and layer take is what it allocates."""
+    import re
+    stated = int(re.search(r"\((\d+) bytes per page, KV head and layer\)", kvq.BlockBounds.alloc.__doc__)[1])
+    codes, scale = _new_bounds(1)
+    assert stated * 2 == codes.numel() * codes.element_size() + scale.numel() * scale.element_size()
+
+
+def test_stated_widest_page_table():
+    """The width that the header states is the last one whose scores fit the kernel's shared memory
+    (its sizes, restated: 4 bytes a page in whole 128s and 8 words, 16 rows of 256 bytes and a factor)."""
+    import os
+    import re
+    here = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(here, "include", "kvq.h")) as f:
+        stated = int(re.search(r"max_pages_per_seq up to ([\d,]+)", f.read())[1].replace(",", ""))
+
+    def fits(pages):
+        return ((pages + 127) // 128 * 128 + 8) * 4 + 16 * (256 + 4) <= 200 * 1024
+
+    assert fits(stated) and not fits(stated + 1)
