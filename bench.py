@@ -485,16 +485,34 @@ def run_kvq(args, rank, world, local_rank):
     return line
 
 
+CSRC = os.path.join(ROOT, "bit_paged_kv_diag_b200", "csrc")
+
+
+def source_hash(name, csrc=CSRC):
+    """Hash of a kernel source and of every header of this repository that it includes, without
+    comments and spacing: what the compiled kernel depends on."""
+    import hashlib
+    import re
+    seen, todo, h = set(), [os.path.join(csrc, name)], hashlib.sha256()
+    while todo:
+        path = os.path.normpath(todo.pop(0))
+        if path in seen:
+            continue
+        seen.add(path)
+        with open(path) as f:
+            text = re.sub(r"//[^\n]*|/\*.*?\*/", " ", f.read(), flags=re.S)
+        todo += [os.path.join(os.path.dirname(path), x) for x in re.findall(r'#include "([^"]+)"', text)]
+        h.update(" ".join(text.split()).encode() + b"\0")
+    return h.hexdigest()[:16]
+
+
 def _traffic(kernel, alg_bytes):
     """DRAM bytes per launch from the committed ncu summary, if it is for the current
     kernel source; else None."""
-    import hashlib
     try:
         with open(os.path.join(ROOT, "profiles", "traffic.json")) as f:
             rec = json.load(f)[kernel]
-        src = os.path.join(ROOT, "bit_paged_kv_diag_b200", "csrc", rec["source"])
-        h = hashlib.sha256(open(src, "rb").read()).hexdigest()[:16]
-        if h != rec["source_sha256_16"]:
+        if source_hash(rec["source"]) != rec["source_sha256_16"]:
             return None
         return int(rec["dram_bytes_per_launch"])
     except Exception:

@@ -396,7 +396,8 @@ class BlockBounds:
         """Addresses for a call on ``cache``.  Both tensors were checked when they were set; they
         are checked again when their data has moved since."""
         codes, scale = self._codes, self._scale
-        if (codes.data_ptr(), scale.data_ptr()) != self._ptrs:
+        at = self._ptrs
+        if codes.data_ptr() != at[0] or scale.data_ptr() != at[1]:
             self._take(codes, scale)
         if self._shape != cache.page_shape:
             raise ValueError(f"bounds of {self._shape} for a cache of {cache.page_shape}")
@@ -514,7 +515,7 @@ def gather_rows(cache: Cache, layer: int, cu_rows, starts, page_table, total_row
                 k_out=None, v_out=None, stream=None):
     """Cached K and V rows in the model's basis: positions starts[b] .. starts[b] + cu_rows[b+1] -
     cu_rows[b] - 1 of every sequence, as two tensors [total_rows][Hkv][128] of ``dtype`` (fp16
-    unless given; bf16)."""
+    unless given; bf16).  Always both; the C call can leave out either."""
     dtype = _torch.float16 if dtype is None else dtype
     code = _dtype_code(dtype)
     shape = (int(total_rows), cache.kv_heads, 128)
