@@ -56,8 +56,6 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "append_row.cuh"
 #include "kvq_internal.h"
 #include "kvq_ptx.cuh"
@@ -143,6 +141,34 @@ __device__ __forceinline__ Dest pair_dest(const AppendParams& p, int gp, uint32_
     d.slot = pos & (p.page_size - 1);
   }
   return d;
+}
+
+// A finished row to its place in the pool: the lane's 32 code bytes (c0, c1) and the row's scale;
+// a bad position or page is flagged and not stored.
+template <bool FP4>
+__device__ __forceinline__ void store_row(const AppendParams& p, const Dest& dcur, int kv, int l, uint4 c0, uint4 c1,
+                                          uint32_t sbits) {
+  const bool bad_pos = dcur.slot < 0;
+  if (bad_pos || dcur.page < 0 || dcur.page >= p.num_pages) {
+    if (l == 0 && kv == 0)
+      atomicOr(p.status, bad_pos ? KVQ_DEV_BAD_POS_BIT : KVQ_DEV_BAD_PAGE_BIT);
+  } else {
+    const int S = p.page_size;
+    constexpr int kScaleBytes = FP4 ? kD / 16 : 2;  // per token row
+    uint8_t* blk = p.pool_layer + (static_cast<size_t>(dcur.page) * p.num_kv_heads + dcur.h) *
+                                      (static_cast<size_t>(S) * (kD + 2 * kScaleBytes));
+    uint4* crow = reinterpret_cast<uint4*>(blk + static_cast<size_t>(kv) * S * (kD / 2) +
+                                           static_cast<size_t>(dcur.slot) * (kD / 2) + 32 * l);
+    crow[0] = c0;
+    crow[1] = c1;
+    uint8_t* srow = blk + static_cast<size_t>(S) * kD + static_cast<size_t>(kv) * S * kScaleBytes +
+                    static_cast<size_t>(dcur.slot) * kScaleBytes;
+    if constexpr (FP4) {
+      *reinterpret_cast<uint32_t*>(srow + 4 * l) = sbits;
+    } else {
+      if (l == 0) *reinterpret_cast<uint16_t*>(srow) = static_cast<uint16_t>(sbits);
+    }
+  }
 }
 
 template <int BLOCK, bool FP4>
@@ -245,56 +271,118 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kernel(AppendPara
         griddep_wait();
         waited = true;
       }
-      const bool bad_pos = dcur.slot < 0;
-      if (bad_pos || dcur.page < 0 || dcur.page >= p.num_pages) {
-        if (l == 0 && kv == 0)
-          atomicOr(p.status, bad_pos ? KVQ_DEV_BAD_POS_BIT : KVQ_DEV_BAD_PAGE_BIT);
-      } else {
-        const int S = p.page_size;
-        constexpr int kScaleBytes = FP4 ? kD / 16 : 2;  // per token row
-        uint8_t* blk = p.pool_layer + (static_cast<size_t>(dcur.page) * p.num_kv_heads + dcur.h) *
-                                          (static_cast<size_t>(S) * (kD + 2 * kScaleBytes));
-        uint4* crow = reinterpret_cast<uint4*>(blk + static_cast<size_t>(kv) * S * (kD / 2) +
-                                               static_cast<size_t>(dcur.slot) * (kD / 2) + 32 * l);
-        crow[0] = c0;
-        crow[1] = c1;
-        uint8_t* srow = blk + static_cast<size_t>(S) * kD + static_cast<size_t>(kv) * S * kScaleBytes +
-                        static_cast<size_t>(dcur.slot) * kScaleBytes;
-        if constexpr (FP4) {
-          *reinterpret_cast<uint32_t*>(srow + 4 * l) = sbits;
-        } else {
-          if (l == 0) *reinterpret_cast<uint16_t*>(srow) = static_cast<uint16_t>(sbits);
-        }
-      }
+      store_row<FP4>(p, dcur, kv, l, c0, c1, sbits);
     }
     dcur = dnext;
   }
 }
 
+// The same for a call of at most one warp stage per warp and one CTA per SM (decode steps, short
+// chunks), where a launch is a chain of latencies: the rows are copied and quantised before the wait
+// for the previous kernel, under its tail.  That kernel may be the one that writes these rows (a
+// read-back, say), so a warp of its own waits and copies them again, next to the arithmetic where
+// there is nothing to wait for; a stage is stored if both copies are the same, and otherwise done again
+// on the second.  An append and a decode in turn (16 x 4096 tokens, in a graph): 25.7 us; with the copies
+// after the wait 28.4; with no second copy, right only if no kernel of this library writes the rows, 24.5.
 template <int BLOCK, bool FP4>
-int launch_block(const cudaLaunchConfig_t& cfg, const AppendParams& p) {
-  // The shared-memory opt-in is an attribute of the function in the current device's
-  // context: set it once per device (devices 64 and up set it on every launch).
-  static std::atomic<unsigned long long> attr_set{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -2;
-  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
-  if (bit == 0 || (attr_set.load(std::memory_order_acquire) & bit) == 0) {
-    if (cudaFuncSetAttribute(append_kernel<BLOCK, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes) != cudaSuccess)
-      return -2;
-    attr_set.fetch_or(bit, std::memory_order_release);
+__global__ void __launch_bounds__(kThreads + 32, 1) append_few_kernel(AppendParams p) {
+  griddep_launch_dependents();
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int npairs = p.total_new_tokens * p.num_kv_heads;
+  const int nws = (npairs + kPairs - 1) / kPairs;
+  const uint64_t pol = l2_policy_evict_first();
+  // Warp ww's region, as in append_kernel: slots 0 and 1 take the first and the second copy.
+  auto region = [&](int ww) { return smem_addr(smem) + ww * kWarpBytes; };
+  constexpr int kCursors = kStages * kSlotBytes + 2 * kPairs * kStgStride, kBars = kCursors + kCursorBytes;
+  const int j = blockIdx.x * kWarps + w;
+  const bool have = w < kWarps && j < nws;
+  if (have && lane == 0) {
+    mbar_init(region(w) + kBars, 1);
+    mbar_init(region(w) + kBars + 8, 1);
+    fence_mbar_init();
+    issue_stage(p, j, npairs, region(w), region(w) + kBars, pol);
   }
+  __syncthreads();
+  if (w == kWarps) {
+    griddep_wait();
+    const int jj = blockIdx.x * kWarps + lane;
+    if (lane < kWarps && jj < nws)
+      issue_stage(p, jj, npairs, region(lane) + kSlotBytes, region(lane) + kBars + 8, pol);
+    return;
+  }
+  if (!have) return;
+
+  const int l = lane & 1, rho = lane & 7, pr = lane >> 2, kv = (lane >> 1) & 1;
+  const unsigned pmask = 0x3u << (lane & 30);
+  const uint32_t ring = region(w), bar0 = ring + kBars, cursor = ring + kCursors + 16 * pr;
+  const uint32_t stg_row = ring + kStages * kSlotBytes + (lane >> 1) * kStgStride + 32 * l;
+  const uint32_t row = ring + kv * kHalfBytes + pr * (kD * 2) + l * kD;  // of the first copy
+  if ((lane & 3) == 0)  // an empty range: the lookup searches
+    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(cursor), "r"(0u) : "memory");
+  __syncwarp();
+  const bool active = j * kPairs + pr < npairs;
+  Dest d = {-1, -1, 0};
+  if (active) d = pair_dest(p, j * kPairs + pr, cursor);
+  bool late = !mbar_wait_warp(bar0, 0u, kWaitLimitNs);
+  uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0;
+  uint32_t sbits = 0u;
+#pragma unroll 1
+  for (int copy = 0; !late; copy++) {
+    if (active) {  // both lanes of a row, and both rows of a pair, take the same branch
+      uint4 raw[8];
+#pragma unroll
+      for (int t = 0; t < 8; t++) raw[t] = lds_128(row + copy * kSlotBytes + 16 * (t ^ rho));
+      f2 x[32];
+      rotate_row<BLOCK>(raw, rho, l, pmask, x);
+      uint32_t q[8];
+      if constexpr (FP4) sbits = quantise_fp4(x, p.cb, rho, q);
+      else sbits = quantise(x, p.cb, pmask, q);
+#pragma unroll
+      for (int t = 0; t < 8; t++) sts_32(stg_row + 4 * (t ^ rho), q[t]);
+      c0 = lds_128(stg_row);
+      c1 = lds_128(stg_row + 16);
+    }
+    if (copy) break;
+    griddep_wait();
+    late = !mbar_wait_warp(bar0 + 8, 0u, kWaitLimitNs);
+    uint32_t diff = 0u;
+    if (active) {
+#pragma unroll
+      for (int t = 0; t < 8; t++) {
+        const uint4 a = lds_128(row + 16 * (t ^ rho)), b = lds_128(row + kSlotBytes + 16 * (t ^ rho));
+        diff |= (a.x ^ b.x) | (a.y ^ b.y) | (a.z ^ b.z) | (a.w ^ b.w);
+      }
+    }
+    if (!__any_sync(0xffffffffu, diff != 0u)) break;
+  }
+  if (late) {
+    // A copy did not land in time: as in append_kernel.
+    if (lane == 0) atomicOr(p.status, KVQ_DEV_TIMEOUT_BIT);
+    mbar_wait_warp(bar0, 0u, kWaitLimitNs);
+    mbar_wait_warp(bar0 + 8, 0u, kWaitLimitNs);
+    return;
+  }
+  if (active) store_row<FP4>(p, d, kv, l, c0, c1, sbits);
+}
+
+template <int BLOCK, bool FP4>
+int launch_block(const cudaLaunchConfig_t& cfg, const AppendParams& p, bool few) {
+  if (few) {
+    if (!ensure_smem<append_few_kernel<BLOCK, FP4>>(kSmemBytes)) return -2;
+    return cudaLaunchKernelEx(&cfg, append_few_kernel<BLOCK, FP4>, p) == cudaSuccess ? 0 : -2;
+  }
+  if (!ensure_smem<append_kernel<BLOCK, FP4>>(kSmemBytes)) return -2;
   return cudaLaunchKernelEx(&cfg, append_kernel<BLOCK, FP4>, p) == cudaSuccess ? 0 : -2;
 }
 
 template <bool FP4>
-int launch_format(const cudaLaunchConfig_t& cfg, const AppendParams& p, int block) {
+int launch_format(const cudaLaunchConfig_t& cfg, const AppendParams& p, int block, bool few) {
   switch (block) {
-    case 1: return launch_block<1, FP4>(cfg, p);
-    case 32: return launch_block<32, FP4>(cfg, p);
-    case 64: return launch_block<64, FP4>(cfg, p);
-    case 128: return launch_block<128, FP4>(cfg, p);
+    case 1: return launch_block<1, FP4>(cfg, p, few);
+    case 32: return launch_block<32, FP4>(cfg, p, few);
+    case 64: return launch_block<64, FP4>(cfg, p, few);
+    case 128: return launch_block<128, FP4>(cfg, p, few);
     default: return -1;
   }
 }
@@ -310,9 +398,10 @@ int launch_append(const AppendParams& p, int block, int num_sms, cudaStream_t st
   const long long full = static_cast<long long>(kCtasPerSm) * num_sms;
   const long long need = (nws + kWarps - 1) / kWarps;
   const long long grid = need < full ? need : full;
+  const bool few = need <= num_sms;  // at most a warp stage per warp and a CTA per SM
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(few ? kThreads + 32 : kThreads);  // (and the warp that copies again)
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -320,7 +409,7 @@ int launch_append(const AppendParams& p, int block, int num_sms, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.fp4 ? launch_format<true>(cfg, p, block) : launch_format<false>(cfg, p, block);
+  return p.fp4 ? launch_format<true>(cfg, p, block, few) : launch_format<false>(cfg, p, block, few);
 }
 
 }  // namespace kvq

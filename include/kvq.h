@@ -76,8 +76,8 @@
  *     its dependents start.  Kernels that do not use programmatic launch (PyTorch's,
  *     cuBLAS's, copies) only do so by completing, and this library's own kernels never write
  *     these arrays.  The calls from kvq_rope_quant_append to kvq_sparse_attention wait before
- *     they read anything.  (The fused append + decode looks at k_new and v_new early, and
- *     again after the wait; only what it finds then counts.)
+ *     they read anything.  (Short appends and the fused append + decode look at the new rows
+ *     early, and again after the wait; only what they find then counts.)
  *   * The current device must be the one the handle was made on; the calls from
  *     kvq_rope_quant_append to kvq_sparse_attention return KVQ_EINVAL otherwise.
  */

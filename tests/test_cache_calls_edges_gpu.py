@@ -34,14 +34,13 @@ def test_tensors_set_again_between_calls():
     assert s.status() == 0
 
 
-@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("n,fused", [(1, True), (1, False), (19, False), (700, False)])
 @pytest.mark.parametrize("fmt", [0, 1])
-def test_outputs_of_a_call_feed_an_append(fused, fmt):
+def test_outputs_of_a_call_feed_an_append(n, fused, fmt):
     """q' of the rotating append, attention outputs and rows read back are the k and v of an append
     or of a fused step that follows at once on the stream."""
     import torch
     B, hkv = 6, 4
-    n = 1 if fused else 700
     s = Setup([900, 40, 0, 333, 2000, 17], [n] * B, hkv, 1, 64, 64, fmt, layers=2, layer=0).fill()
     kvq, cu, lens, after = s.kvq, s.dev(s.cu), s.dev(s.before), s.dev(s.after)
     x, y = (torch.randn(s.T, hkv, D, device="cuda").half() for _ in range(2))
