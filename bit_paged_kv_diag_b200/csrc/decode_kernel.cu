@@ -720,13 +720,13 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(DecodeParams p) {
   int consumed = 0;   // tiles of this warp consumed (tile t uses slot t % kStages)
   bool dead = false;  // a bounded wait gave up: stop touching the ring
   // uf's and ul's q rows: every warp rotates and slices its share of the queries.
-  // (A wait that gave up joins the CTA at the barrier; until then it works on whatever is there.)
-  const bool q_late = !mbar_wait_bounded(qbar_cta, 0u, kWaitLimitNs);
-  for (int t = 0; t < (two_edges ? 2 : 1); t++)
-    prep_q<G, kWarps, FP4>(qraw_all + (kWarps + t) * G * kD * 2, frag_all + (kWarps + t) * kFragWords,
-                           sf_all + (kWarps + t) * 8, lane, p, w);
-  dead = __syncthreads_or(q_late);
+  if (!mbar_wait_warp(qbar_cta, 0u, kWaitLimitNs)) dead = true;
+  if (!dead)
+    for (int t = 0; t < (two_edges ? 2 : 1); t++)
+      prep_q<G, kWarps, FP4>(qraw_all + (kWarps + t) * G * kD * 2, frag_all + (kWarps + t) * kFragWords,
+                             sf_all + (kWarps + t) * 8, lane, p, w);
   if (dead && lane == 0) atomicOr(p.status, KVQ_DEV_TIMEOUT_BIT);
+  __syncthreads();
   if constexpr (FUSED) {
     if (pre_quantised &&
         __any_sync(kFull, kraw0.x != kraw1.x || kraw0.y != kraw1.y || vraw0.x != vraw1.x || vraw0.y != vraw1.y))
