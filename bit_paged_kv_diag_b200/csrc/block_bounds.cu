@@ -6,7 +6,7 @@
 // fp16).  With a = max_d max(|mx_d|, |mn_d|), sigma is the least power of two with 127 sigma >= a
 // (0 when a = 0) and hi_d = ceil(mx_d / sigma), lo_d = floor(mn_d / sigma) are int8: outward, so
 // that lo_d sigma <= k_d <= hi_d sigma holds for every key of the page and a score from the
-// bounds is never below a key's own.  A power of two keeps both divisions exact.
+// bounds is never below a key's own with the same query (which the page choice rounds to int8).  A power of two keeps both divisions exact.
 //
 // Layout.  One warp per (page, head); the page's key codes and scales come by bulk copies of up to
 // 64 rows into the warp's own two shared-memory slots (loaded straight into registers, the
@@ -15,8 +15,8 @@
 // so that each nibble expansion yields one channel of two rows and the running bounds take
 // three-operand minima and maxima; the halves meet once at the end.
 //
-// Measured: 8 x 8192 INT4 tokens in pages of 64, 8 heads: 19.8 us for 38 MB (5.8 us at the copy
-// rate); the arithmetic pipe (conversions, minima, maxima) is busy for 61 % of it.  The last pages
+// Measured, the kernel alone behind a flush of L2: 8 x 8192 INT4 tokens in pages of 64, 8 heads: 19.5
+// us for 38 MB (5.8 us at the copy rate); the arithmetic pipe (conversions, minima, maxima) is busy for 60 % of it.  The last pages
 // of 256 sequences: 7.0 us, a chain of four memory round trips.
 #include <cuda_fp16.h>
 #include <math_constants.h>

@@ -1,5 +1,5 @@
 // block_select.cu -- the pages that each query and KV head attends, chosen by an upper bound of
-// q.k over the page's keys, for sm_100a.
+// q.k over the page's keys, q rounded to int8, for sm_100a.
 //
 // Mathematics.  Every query head's q is rotated with the cache's transform (y = c_b * butterfly,
 // fp32, fixed order) and cut to int8: s = fl(max_d |y_d| / 127), c_d = rint(fl(y_d / s)), 0 when
@@ -28,11 +28,15 @@
 // 20 passes over the keys).  The
 // pages are then written in ascending order from ballot masks.  A team of warps shares a query.
 //
-// Measured: 464 queries, 8 KV heads, G = 4, up to 1024 pages: 37 us in one wave of 264 CTAs, about
+// Measured, the kernel alone behind a flush of L2: 464 queries, 8 KV heads, G = 4, up to 1024 pages, on
+// a page table of that width: 37 us in one wave of 264 CTAs, about
 // a third each for q's codes, the scores and the choice, all of it dependency chains (16 warps per
 // SM at 128 registers, 43 % of the issue slots; the integer MMAs are busy for 20 %).
 // One decode step of 4 sequences of up to 2048 pages, 4 KV heads, G = 8: 12 us, of which the launch
 // and the memory round trips to the first page rows are half.
+// The tile and the cluster are planned from the width of the page table, all that the host knows: a
+// wider table leaves fewer queries a tile.  The same chunk on tables of 2048, 4096 and 8192 pages: 1.06,
+// 1.5 and 2.7 times the time; the decode step on 8192: 1.01 times.
 //
 // Few queries: a cluster of up to 8 CTAs shares the pages of one tile, and its first CTA collects
 // the keys through distributed shared memory and makes the choice.

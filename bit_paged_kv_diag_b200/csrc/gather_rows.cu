@@ -17,7 +17,7 @@
 // the chunk (8 channels) t ^ 4 l, so that with rows 272 bytes apart the lanes' 16-byte stores hit
 // all banks evenly; the stage h = 32 and the exchange of h = 64 account for that order.
 //
-// Measured: 65,536 INT4 tokens x 8 heads (b = 128) 72 us, 4.7 TB/s; 161,700 NVFP4 tokens x 4 heads
+// Measured, the kernel alone behind a flush of L2: 65,536 INT4 tokens x 8 heads (b = 128) 72 us, 4.7 TB/s; 161,700 NVFP4 tokens x 4 heads
 // (b = 64) 84 us, 5.0 TB/s -- 0.72 and 0.77 of the copy rate.  The arithmetic pipe is busy for 57 %
 // of the time, the issue slots for 65 %.  Stores straight from registers took 95 and 103 us, one of
 // K and V per warp 86 and 90 us.

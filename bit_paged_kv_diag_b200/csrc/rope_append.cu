@@ -7,8 +7,9 @@
 // with (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) for the interleaved form.  The angle
 // is formed in fp64 because an fp32 product of a far position loses the angle itself (2^17
 // tokens times 1 leaves 2^-7 radian).  For k both products and the sum round to fp32 one by one,
-// so that the stored codes are those of any implementation that rounds the same way; k' stays in
-// fp32 on its way into the block-diagonal Hadamard butterfly and the quantiser (append_row.cuh),
+// so that the stored codes are those of any implementation that rounds the same way from the same
+// cosines and sines (these may round apart by a step of fp32, which moves at most one code in 10^5 by
+// one); k' stays in fp32 on its way into the block-diagonal Hadamard butterfly and the quantiser (append_row.cuh),
 // which are the append kernel's.  For q the sum is one fma; q' is rounded once to fp16, the type
 // that the attention calls read.
 //
@@ -21,13 +22,15 @@
 //      each computing both partners' products, cost 77).
 //   k, v: two lanes a row, as in the append kernel.  (Eight lanes a row straight from global memory
 //      repeat the scale's divisions and the addresses four times as often: 349 us against 303.)
-// Measured, 8 x 8192 tokens, 32 + 2 x 8 heads, INT4, b = 128: 262 us, 5.4 TB/s of algorithmic
+// Measured, the kernel alone behind a flush of L2, 8 x 8192 tokens, 32 + 2 x 8 heads, INT4, b = 128:
+// 262 us, 5.4 TB/s of algorithmic
 // bytes, 0.82 of the copy rate; 132 M warp instructions at 46 % of the issue slots with 16 warps per
 // SM.  One token for each of 16 sequences: 7.9 us, of which about 2 us are the chain of offsets,
 // length and page, and much of the rest instruction fetches: the form of the pairs is a template
 // parameter because the smaller code took 9.0 us down to 7.9 (and 274 to 262).  Not kept: one
 // persistent CTA per slot with the next tile's copies in flight (registers spill: 503 us); copies
 // issued only after the tokens' places are known (352 us); q rows loaded a stage ahead (266 us).
+// (NVFP4 with b = 128 spills 4 to 8 bytes at the 128 registers of four CTAs per SM.)
 #include <cuda_fp16.h>
 #include <stdint.h>
 

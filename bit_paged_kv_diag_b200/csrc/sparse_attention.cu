@@ -16,11 +16,14 @@
 // in the handle's scratch and the last to arrive merges them in the order of the parts, so the
 // result does not depend on the order of arrival.
 //
-// Measured: 16 sequences x 8 KV heads, G = 4, INT4, 4096 tokens each: 24.6 us, 2.8 TB/s (a plain
-// stream of these 69 MB takes 14 us; the dense decode of the same bytes 22.4 us); 951 queries x 4
-// KV heads, G = 8, NVFP4, 1024 tokens each: 199 us, 2.8 TB/s out of L2.  Bound by instructions:
-// about 530 a tile (INT4, G = 4) and 870 (NVFP4, G = 8), most of them dequantisation, at 50 and
-// 62 % of the issue slots; four CTAs per SM are 4 % faster than three with a deeper ring.
+// Measured, the kernel alone behind a flush of L2: 16 sequences x 8 KV heads, G = 4, INT4, 4096 tokens
+// each: 25.0 us, 2.8 TB/s (a plain stream of these 69 MB takes 14 us; the dense decode of the same
+// bytes, back to back in a graph, 22.4 us); 951 queries x 4 KV heads, G = 8, NVFP4, 1024 tokens each: 201
+// us, 2.8 TB/s out of L2.  Bound by instructions: about 530 a tile (INT4, G = 4) and 870 (NVFP4, G = 8),
+// most of them dequantisation, at 51 and 61 % of the issue slots.  Four CTAs per SM were 4 % faster than
+// three with a deeper ring although their 128 registers spill at G = 8 (stored / loaded bytes: NVFP4 156 /
+// 120 with tiles of one page, 12 / 12 with two; INT4 44 / 32 and 80 / 116) and a little with tiles of two
+// pages at G = 1 (INT4, 12 / 36) and G = 2 (NVFP4, 4 / 4); G = 4 does not.
 #include <cuda_fp16.h>
 #include <math_constants.h>
 #include <stdint.h>

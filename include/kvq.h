@@ -332,7 +332,8 @@ KVQ_API int kvq_update_block_bounds(kvq_cache* c, int32_t layer, void* codes, fl
                                     int32_t total_new_tokens, void* stream);
 
 /* Pages to attend, per query and KV head: the first `sink` and the last `recent` pages at or
- * before the query's position, and of the others those with the largest upper bound of q.k,
+ * before the query's position, and of the others those with the largest upper bound of q.k over
+ * the page's keys, q rounded to int8 (c s below; with q itself a key can lie above it by s/2 sum |k_d|),
  *   score = max over the KV head's query heads g of fl32(I_g s_g) * sigma,
  *   I_g = sum_d max(c_d, 0) hi_d + min(c_d, 0) lo_d,
  * where c = rint(y / s), s = fl32(max |y| / 127), y = q rotated with the cache's transform; a
