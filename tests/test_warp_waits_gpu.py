@@ -57,7 +57,7 @@ def test_all_lanes_get_the_same_answer(tmp_path):
     assert not answers.any()
     # Arrivals from long before to long after the limit.
     for _ in range(5):
-        assert run(answers.data_ptr(), blocks, 50000, 50) == 0
+        assert run(answers.data_ptr(), blocks, 200000, 200) == 0
         a = answers.cpu().numpy()
         assert (a == a[:, :1]).all() and np.isin(a, (0, 1)).all()
         assert a[0].all() and not a[-1].any()
